@@ -353,6 +353,137 @@ moe_status moe_check_routing(const int32_t* topk_ids, int32_t T, int32_t k, int3
                              int32_t* result, void* stream);
 
 /* ------------------------------------------------------------------ */
+/* Router statistics, losses and gradient.                              */
+/* ------------------------------------------------------------------ */
+
+/*
+ * moe_balance_loss: how evenly a batch's routing uses the experts, per
+ * sequence s with the n_s counting tokens t in it and p_t = softmax(scores[t]):
+ *   counts[s][e] = number of (t, j) with topk_ids[t][j] = e
+ *   tokens[s]    = n_s
+ *   loss[s][0]   = sum_e f_e P_e with f_e = E counts[s][e] / (k n_s) and
+ *                  P_e = (1/n_s) sum_t p_t[e]    (1 for an even routing)
+ *   loss[s][1]   = (1/n_s) sum_t lse(scores[t])^2        (the z loss)
+ * A sequence without a counting token has counts 0 and losses 0.
+ *   scores      device [T][E] float32; -inf takes an expert out of the softmax,
+ *               a token with no other score does not count
+ *   topk_ids    device [T][k] int32 (moe_topk_route's)
+ *   token_mask  device [T] bytes or NULL: a token with a 0 does not count, its
+ *               scores and ids are not read
+ *   seq_offsets device [S+1] int32, ascending in [0, T] (read clamped to it):
+ *               sequence s is tokens seq_offsets[s] .. seq_offsets[s+1] - 1 and
+ *               may be empty; tokens before the first and behind the last
+ *               sequence do not count.  NULL (S = 1 only): all tokens
+ *   counts device [S][E] int32, tokens device [S] int32, loss device [S][2] float32
+ *   workspace   device, >= moe_balance_workspace_bytes(T, E, S), 16-byte aligned
+ *               (NULL if that is 0)
+ * All sums are FP32 in an order that depends on the sizes only: equal inputs
+ * give equal bits.  T == 0 writes zeros.
+ * Sizes: 0 <= T <= 2^30, 1 <= E <= 1024, 1 <= k <= min(E, 64), 1 <= S <= 2^20,
+ * T*k <= 2^31 - 1.  Errors: MOE_ERR_INVALID_ARG for bad sizes and null or
+ * misaligned pointers, MOE_ERR_UNSUPPORTED for sizes past the limits.
+ */
+size_t moe_balance_workspace_bytes(int32_t T, int32_t E, int32_t S);
+
+moe_status moe_balance_loss(const float* scores, const int32_t* topk_ids,
+                            const uint8_t* token_mask, const int32_t* seq_offsets, int32_t T,
+                            int32_t E, int32_t k, int32_t S, int32_t* counts, int32_t* tokens,
+                            float* loss, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_router_backward: the gradient of the scores,
+ *   grad_scores[t][e] = p_te / n_s (grad_loss[s][0] (f_e - sum_i f_i p_ti)
+ *                                   + 2 grad_loss[s][1] lse(scores[t]))
+ *                     + sum_{j: topk_ids[t][j] = e} w_tj (dw_tj - sum_i w_ti dw_ti)
+ * the first line for the tokens that count in moe_balance_loss (counts are
+ * constants of it), the second, through moe_topk_route's weights w, for every
+ * token.  Every element is written, with 0 where neither reaches.
+ *   grad_loss    device [S][2] float32, or NULL: no first line (counts, tokens,
+ *                token_mask, seq_offsets and scores are then not read)
+ *   counts, tokens  from moe_balance_loss on the same inputs
+ *   topk_weights, grad_weights  device [T][k] float32, or both NULL: no second line
+ *                (topk_ids is then not read)
+ *   grad_scores  device [T][E] float32
+ * T == 0 is a no-op.  Sizes and errors as moe_balance_loss; with both
+ * grad_loss and grad_weights NULL MOE_ERR_INVALID_ARG.
+ */
+moe_status moe_router_backward(const float* scores, const int32_t* topk_ids,
+                               const float* topk_weights, const float* grad_weights,
+                               const uint8_t* token_mask, const int32_t* seq_offsets,
+                               const int32_t* counts, const int32_t* tokens,
+                               const float* grad_loss, int32_t T, int32_t E, int32_t k, int32_t S,
+                               float* grad_scores, void* stream);
+
+/* ------------------------------------------------------------------ */
+/* Norms before and after a block, with its gate and residual scale.    */
+/* ------------------------------------------------------------------ */
+
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1, /* gate [H], x_dtype     */
+  MOE_GATE_TOKEN = 2,   /* gate [T], float32     */
+  MOE_GATE_FULL = 3     /* gate [T][H], x_dtype  */
+} moe_gate_kind;
+
+/* A block's join with the residual stream.  A host struct of device pointers. */
+typedef struct {
+  int32_t T, H;
+  int32_t x_dtype;          /* x, out, n, weights, their gradients' rows: MOE_DT_*   */
+  int32_t y_dtype;          /* y and its gradient: x_dtype or MOE_DT_F32             */
+  int32_t gate_kind;        /* moe_gate_kind                                         */
+  float res_scale, eps;
+  int64_t x_stride, y_stride; /* elements from a row of x / y to the next, >= H      */
+  const void* x;            /* [T][H]: the residual stream                           */
+  const void* y;            /* [T][H]: the block's output, or NULL: no join          */
+  const void* w_post;       /* [H] x_dtype: weight of y's norm, or NULL: y as it is  */
+  const void* w_next;       /* [H] x_dtype: weight of the next norm, or NULL: none   */
+  const void* gate;         /* by gate_kind, NULL for MOE_GATE_NONE                  */
+} moe_block;
+
+/*
+ * moe_block_norm: with rms(v) = sqrt(mean v^2 + eps) over a row,
+ *   out_t = res_scale x_t + gate_t (.) ( y_t / rms(y_t) (.) w_post )
+ *   n_t   = out_t / rms(out_t) (.) w_next
+ * in one pass: the norm after a block, its gate and residual join, and the
+ * norm before the next block.  Without y it is that last norm alone: n of x.
+ *   out  device [T][H] x_dtype, contiguous; NULL exactly when y is NULL.  It may
+ *        be x itself when x_stride == H
+ *   n    device [T][H] x_dtype, contiguous; NULL exactly when w_next is NULL
+ * Statistics and sums are FP32; out and n are rounded once each, n from the
+ * unrounded out.  The mean square of a row must be finite in FP32; with eps 0
+ * a zero row gives NaN.  T == 0 is a no-op.
+ * Sizes: 1 <= H <= 16384 (MOE_ERR_UNSUPPORTED past it), eps >= 0.  Rows are
+ * read 16 bytes at a time when H and the strides are multiples of 8 and the
+ * pointers 16-byte aligned, by element otherwise.
+ */
+moe_status moe_block_norm(const moe_block* B, void* out, void* n, void* stream);
+
+/*
+ * moe_block_norm_backward: the gradients of moe_block_norm's inputs from
+ * grad_out and grad_n (x_dtype [T][H] contiguous).  B is the forward call's
+ * with one difference: B->x is the stored `out` (x itself without y).  It is
+ * read only for the next norm and may be NULL without w_next.
+ *   grad_out    NULL: 0;  grad_n: given exactly when w_next is
+ *   grad_x      device [T][H] x_dtype contiguous
+ *   grad_y      device [T][H] y_dtype contiguous, given exactly when y is
+ *   grad_gate   by gate_kind: [H] float32, [T] float32, [T][H] x_dtype; NULL for
+ *               MOE_GATE_NONE
+ *   grad_w_post, grad_w_next  device [H] float32, given exactly when the weights
+ *               are: sums over the tokens, in FP32, in an order that depends on
+ *               the sizes only (T == 0 writes zeros)
+ *   workspace   device, >= moe_block_norm_backward_workspace_bytes(T, H) bytes,
+ *               16-byte aligned; no contents kept between calls
+ * Without y and without w_next there is nothing to differentiate:
+ * MOE_ERR_INVALID_ARG.
+ */
+size_t moe_block_norm_backward_workspace_bytes(int32_t T, int32_t H);
+
+moe_status moe_block_norm_backward(const moe_block* B, const void* grad_out, const void* grad_n,
+                                   void* grad_x, void* grad_y, void* grad_gate,
+                                   float* grad_w_post, float* grad_w_next, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ */
 /* The whole layer.                                                     */
 /* ------------------------------------------------------------------ */
 

@@ -22,6 +22,7 @@ FMT = {"f32": 0, "mxfp8": 1, "mxfp4": 2, "fp8_blk128": 3}
 PATH = {"auto": 0, "decode": 1, "grouped": 2}
 PATH_NAME = {v: k for k, v in PATH.items()}
 DOWN_VARIANT = {"auto": 0, "token": 1, "expert": 2}
+GATE = {"none": 0, "channel": 1, "token": 2, "full": 3}
 
 _lib = None
 
@@ -40,10 +41,22 @@ class _Weights(ctypes.Structure):
                 ("w2", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p)]
 
 
+class _Block(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("gate_kind", ctypes.c_int32),
+                ("res_scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("w_post", ctypes.c_void_p), ("w_next", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _Z = ctypes.c_size_t
 _WP = ctypes.POINTER(_Weights)
+_BP = ctypes.POINTER(_Block)
 
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -61,6 +74,12 @@ _SIGS = {
     "moe_combine": (_I, [_P, _I, _I, _I, _P, _I, _P]),
     "moe_topk_route": (_I, [_P, _P, _I, _I, _I, _P, _P, _P]),
     "moe_check_routing": (_I, [_P, _I, _I, _I, _P, _P]),
+    "moe_balance_workspace_bytes": (_Z, [_I, _I, _I]),
+    "moe_balance_loss": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
+    "moe_router_backward": (_I, [_P] * 9 + [_I, _I, _I, _I, _P, _P]),
+    "moe_block_norm": (_I, [_BP, _P, _P, _P]),
+    "moe_block_norm_backward_workspace_bytes": (_Z, [_I, _I]),
+    "moe_block_norm_backward": (_I, [_BP, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
     "moe_choose_path": (_I, [_WP, _I, _I]),
     "moe_layer_workspace_bytes": (_Z, [_WP, _I, _I, _I, _I]),
     "moe_layer": (_I, [_WP, _P, _I, _P, _P, _I, _I, _P, _I, _I, _I, _P, _Z,
@@ -322,6 +341,210 @@ def check_routing(ids, num_experts, result=None, stream=None):
                                 _ptr(result), _stream(stream))
     _check(st, "moe_check_routing")
     return result
+
+
+# ---- operators around the layer ------------------------------------------
+
+def _on_device(fn):
+    """Run a binding call on its first tensor's device and, with `stream`,
+    with that stream made torch's current one (as _on_stream)."""
+    @functools.wraps(fn)
+    def wrapped(first, *args, stream=None, **kwargs):
+        dev = first.device
+        if dev.type != "cuda":
+            raise ValueError(f"{fn.__name__}: tensors must be on a GPU, not on {dev}")
+        if stream is None and dev.index == torch.cuda.current_device():
+            return fn(first, *args, **kwargs)
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"{fn.__name__}: the stream belongs to {stream.device}, the tensors to {dev}")
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return fn(first, *args, **kwargs)
+    return wrapped
+
+
+def _need(cond, what):
+    if not cond:
+        raise ValueError(what)
+
+
+def _tensor(t, name, like, shape, dtypes):
+    """Data pointer of t (None for None) after its checks: on `like`'s device,
+    contiguous, of that shape and one of those dtypes."""
+    if t is None:
+        return None
+    if t.device != like.device or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor {list(shape)} of {dtypes} on {like.device} is "
+                         f"needed, not {list(t.shape)} {t.dtype} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', strided'}")
+    return t.data_ptr()
+
+
+_F32, _I32 = (torch.float32,), (torch.int32,)
+_BYTES = (torch.uint8, torch.bool)
+
+
+def _sequences(seq_offsets, scores):
+    if seq_offsets is None:
+        return 1, None
+    _need(seq_offsets.dim() == 1 and seq_offsets.shape[0] >= 2, "seq_offsets: [S + 1] with S >= 1")
+    return seq_offsets.shape[0] - 1, _tensor(seq_offsets, "seq_offsets", scores, seq_offsets.shape, _I32)
+
+
+@_on_device
+def balance_loss(scores, ids, mask=None, seq_offsets=None):
+    """Router statistics of scores [T][E] float32 and the routed ids [T][k]:
+    (loss [S][2] float32 -- balance and z loss, counts [S][E] int32, tokens [S]
+    int32).  mask [T] bool: tokens that count; seq_offsets [S+1] int32: the
+    sequences' bounds in T (default: one sequence of all tokens)."""
+    load()
+    _need(scores.dim() == 2 and ids.dim() == 2, "scores [T][E] and ids [T][k] are needed")
+    t, e = scores.shape
+    k = ids.shape[1]
+    s, offs = _sequences(seq_offsets, scores)
+    args = (_tensor(scores, "scores", scores, (t, e), _F32), _tensor(ids, "ids", scores, (t, k), _I32),
+            _tensor(mask, "mask", scores, (t,), _BYTES), offs)
+    loss = torch.empty((s, 2), dtype=torch.float32, device=scores.device)
+    counts = torch.empty((s, e), dtype=torch.int32, device=scores.device)
+    tokens = torch.empty((s,), dtype=torch.int32, device=scores.device)
+    wsb = _lib.moe_balance_workspace_bytes(t, e, s)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=scores.device) if wsb else None
+    st = _lib.moe_balance_loss(*args, t, e, k, s, counts.data_ptr(), tokens.data_ptr(),
+                               loss.data_ptr(), None if ws is None else ws.data_ptr(), wsb,
+                               torch.cuda.current_stream().cuda_stream)
+    _check(st, "moe_balance_loss")
+    return loss, counts, tokens
+
+
+@_on_device
+def router_backward(scores, ids, grad_loss=None, counts=None, tokens=None, mask=None,
+                    seq_offsets=None, weights=None, grad_weights=None, out=None):
+    """Gradient [T][E] float32 of the scores: from grad_loss [S][2] with counts
+    and tokens of balance_loss on the same inputs, and / or from grad_weights
+    [T][k] through the routing weights of topk_route."""
+    load()
+    _need(scores.dim() == 2 and ids.dim() == 2, "scores [T][E] and ids [T][k] are needed")
+    t, e = scores.shape
+    k = ids.shape[1]
+    s, offs = _sequences(seq_offsets, scores)
+    if out is None:
+        out = torch.empty((t, e), dtype=torch.float32, device=scores.device)
+    st = _lib.moe_router_backward(
+        _tensor(scores, "scores", scores, (t, e), _F32), _tensor(ids, "ids", scores, (t, k), _I32),
+        _tensor(weights, "weights", scores, (t, k), _F32),
+        _tensor(grad_weights, "grad_weights", scores, (t, k), _F32),
+        _tensor(mask, "mask", scores, (t,), _BYTES), offs,
+        _tensor(counts, "counts", scores, (s, e), _I32), _tensor(tokens, "tokens", scores, (s,), _I32),
+        _tensor(grad_loss, "grad_loss", scores, (s, 2), _F32), t, e, k, s,
+        _tensor(out, "out", scores, (t, e), _F32), torch.cuda.current_stream().cuda_stream)
+    _check(st, "moe_router_backward")
+    return out
+
+
+_ROWS = {torch.bfloat16: DT["bf16"], torch.float32: DT["f32"]}
+
+
+def _row_stride(x, name):
+    if x.dtype not in _ROWS:
+        raise ValueError(f"{name}: bfloat16 or float32 rows are needed, not {x.dtype}")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1) or \
+            (x.shape[0] > 1 and x.stride(0) < x.shape[1]):
+        raise ValueError(f"{name}: rows [T][H] with consecutive elements are needed")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _block(like, x, y, w_post, w_next, gate, res_scale, eps):
+    t, h = like.shape
+    dts = (like.dtype,)
+    b = _Block()
+    b.T, b.H, b.x_dtype, b.y_dtype = t, h, _ROWS[like.dtype], _ROWS[like.dtype]
+    b.x_stride = b.y_stride = h
+    b.res_scale, b.eps = res_scale, eps
+    if x is not None:
+        b.x, b.x_stride = x.data_ptr(), _row_stride(x, "x")
+    if y is not None:
+        b.y_stride = _row_stride(y, "y")
+        _need(y.shape == like.shape and y.device == like.device, "y: of x's shape and device")
+        b.y, b.y_dtype = y.data_ptr(), _ROWS[y.dtype]
+    b.w_post = _tensor(w_post, "w_post", like, (h,), dts)
+    b.w_next = _tensor(w_next, "w_next", like, (h,), dts)
+    kind = "none"
+    if gate is not None:
+        kind = "channel" if gate.dim() == 1 else "token" if gate.shape[1] == 1 and (
+            h > 1 or gate.dtype == torch.float32) else "full"
+        shape = {"channel": (h,), "token": (t, 1), "full": (t, h)}[kind]
+        b.gate = _tensor(gate, f"gate ({kind})", like, shape, _F32 if kind == "token" else dts)
+    b.gate_kind = GATE[kind]
+    return b, kind
+
+
+@_on_device
+def block_norm(x, y=None, w_post=None, w_next=None, gate=None, res_scale=1.0, eps=1e-6, out=None,
+               n=None):
+    """The norm after a block, its gate and residual join, and the norm before
+    the next block: (out, n) with out = res_scale x + gate (.) norm(y) w_post and
+    n = norm(out) w_next.  Without y: (None, norm(x) w_next).  x, y [T][H] with
+    any row stride; weights [H] and gate [H] (channels) or [T][H] in x's dtype,
+    or gate [T][1] float32 (tokens).  out may be x (in place)."""
+    load()
+    _row_stride(x, "x")
+    b, _ = _block(x, x, y, w_post, w_next, gate, res_scale, eps)
+    if y is None:
+        _need(out is None, "out goes with y")
+    elif out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if w_next is None:
+        _need(n is None, "n goes with w_next")
+    elif n is None:
+        n = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dts = (x.dtype,)
+    st = _lib.moe_block_norm(b, _tensor(out, "out", x, x.shape, dts), _tensor(n, "n", x, x.shape, dts),
+                             torch.cuda.current_stream().cuda_stream)
+    _check(st, "moe_block_norm")
+    return out, n
+
+
+def block_norm_backward(grad_out, grad_n, out, y=None, w_post=None, w_next=None, gate=None,
+                        res_scale=1.0, eps=1e-6, stream=None):
+    """Gradients of block_norm's inputs, a dict of "x", "y", "gate", "w_post"
+    and "w_next" (None where the input was), from grad_out and grad_n (either
+    may be None where it does not reach the loss or does not exist).  out: what
+    block_norm returned (without y: its x)."""
+    like = grad_out if grad_out is not None else grad_n
+    _need(like is not None, "grad_out or grad_n is needed")
+    return _block_norm_backward(like, grad_out, grad_n, out, y, w_post, w_next, gate, res_scale, eps,
+                                stream=stream)
+
+
+@_on_device
+def _block_norm_backward(like, grad_out, grad_n, out, y, w_post, w_next, gate, res_scale, eps):
+    load()
+    _need(like.dtype in _ROWS and like.dim() == 2, "gradients: bfloat16 or float32 rows [T][H]")
+    t, h = like.shape
+    dev, dts = like.device, (like.dtype,)
+    if w_next is not None:
+        _need(out is not None and out.shape == like.shape and out.dtype == like.dtype and
+              out.device == dev, "out: of the gradients' shape, dtype and device")
+        if grad_n is None:
+            grad_n = torch.zeros_like(like)
+    b, kind = _block(like, out if w_next is not None else None, y, w_post, w_next, gate, res_scale, eps)
+    g = {"x": torch.empty_like(like, memory_format=torch.contiguous_format), "y": None, "gate": None,
+         "w_post": None, "w_next": None}
+    if y is not None:
+        g["y"] = torch.empty((t, h), dtype=y.dtype, device=dev)
+    if gate is not None:
+        g["gate"] = torch.empty(gate.shape, dtype=like.dtype if kind == "full" else torch.float32,
+                                device=dev)
+    for name, w in (("w_post", w_post), ("w_next", w_next)):
+        if w is not None:
+            g[name] = torch.empty((h,), dtype=torch.float32, device=dev)
+    wsb = _lib.moe_block_norm_backward_workspace_bytes(t, h)
+    ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
+    st = _lib.moe_block_norm_backward(
+        b, _tensor(grad_out, "grad_out", like, (t, h), dts), _tensor(grad_n, "grad_n", like, (t, h), dts),
+        g["x"].data_ptr(), _ptr(g["y"]), _ptr(g["gate"]), _ptr(g["w_post"]), _ptr(g["w_next"]),
+        ws.data_ptr(), wsb, torch.cuda.current_stream().cuda_stream)
+    _check(st, "moe_block_norm_backward")
+    return g
 
 
 def choose_path(W, t, k):

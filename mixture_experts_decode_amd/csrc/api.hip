@@ -188,6 +188,36 @@ size_t decode_workspace(const moe_weights* W, int32_t T, int32_t k) {
   return decode_h_bytes(W, T, k) + decode_slot_bytes(W, T, k);
 }
 
+// ---- operators around the layer -------------------------------------------
+
+constexpr int32_t kMaxNormH = 16384;        // a row's registers over one workgroup
+constexpr int32_t kMaxBalanceTokens = 1 << 30;
+constexpr int32_t kMaxSequences = 1 << 20;
+
+moe_status check_balance_sizes(int32_t T, int32_t E, int32_t k, int32_t S) {
+  if (T < 0 || E < 1 || E > kMaxExpertsTotal || k < 1 || k > E || k > 64 || S < 1)
+    return MOE_ERR_INVALID_ARG;
+  if (T > kMaxBalanceTokens || S > kMaxSequences || (int64_t)T * k > INT32_MAX)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_block(const moe_block* B) {
+  if (!B || B->T < 0 || B->H < 1 || !dtype_ok(B->x_dtype) || !dtype_ok(B->y_dtype))
+    return MOE_ERR_INVALID_ARG;
+  if (B->gate_kind < MOE_GATE_NONE || B->gate_kind > MOE_GATE_FULL) return MOE_ERR_INVALID_ARG;
+  if (!(B->eps >= 0.0f) || !std::isfinite(B->eps) || !std::isfinite(B->res_scale))
+    return MOE_ERR_INVALID_ARG;
+  // an empty batch has no rows to point to
+  if (B->T > 0 && !B->y && (B->w_post || B->gate_kind != MOE_GATE_NONE))
+    return MOE_ERR_INVALID_ARG;
+  if (B->T > 0 && (B->gate_kind != MOE_GATE_NONE) != (B->gate != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (B->x_stride < B->H || (B->y && B->y_stride < B->H)) return MOE_ERR_INVALID_ARG;
+  if (B->H > kMaxNormH) return MOE_ERR_UNSUPPORTED;
+  if (B->y && B->x_dtype == MOE_DT_F32 && B->y_dtype != MOE_DT_F32) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 // ---- workspace held by the library, for callers that cannot allocate -----
 
 constexpr size_t kScratchBytes = size_t(32) << 20;   // per device
@@ -405,6 +435,98 @@ moe_status moe_check_routing(const int32_t* topk_ids, int32_t T, int32_t k, int3
   if ((int64_t)T * k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   return from_hip(moe::launch_check_routing(topk_ids, T * k, num_experts, result,
                                             as_stream(stream)));
+}
+
+// ---- router statistics, losses and gradient ------------------------------
+
+size_t moe_balance_workspace_bytes(int32_t T, int32_t E, int32_t S) {
+  if (check_balance_sizes(T, E, 1, S) != MOE_OK) return 0;
+  return moe::balance_workspace_bytes(T, E, S);
+}
+
+moe_status moe_balance_loss(const float* scores, const int32_t* topk_ids,
+                            const uint8_t* token_mask, const int32_t* seq_offsets, int32_t T,
+                            int32_t E, int32_t k, int32_t S, int32_t* counts, int32_t* tokens,
+                            float* loss, void* workspace, size_t workspace_bytes, void* stream) {
+  const moe_status st = check_balance_sizes(T, E, k, S);
+  if (st != MOE_OK) return st;
+  if (!counts || !tokens || !loss || (T > 0 && (!scores || !topk_ids))) return MOE_ERR_INVALID_ARG;
+  if (!seq_offsets && S != 1) return MOE_ERR_INVALID_ARG;
+  const size_t need = moe::balance_workspace_bytes(T, E, S);
+  if (need > 0) {
+    if (!workspace) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned16(workspace)) return MOE_ERR_INVALID_ARG;
+  }
+  return from_hip(moe::launch_balance(scores, topk_ids, token_mask, seq_offsets, T, E, k, S,
+                                      counts, tokens, loss, workspace, as_stream(stream)));
+}
+
+moe_status moe_router_backward(const float* scores, const int32_t* topk_ids,
+                               const float* topk_weights, const float* grad_weights,
+                               const uint8_t* token_mask, const int32_t* seq_offsets,
+                               const int32_t* counts, const int32_t* tokens,
+                               const float* grad_loss, int32_t T, int32_t E, int32_t k, int32_t S,
+                               float* grad_scores, void* stream) {
+  const moe_status st = check_balance_sizes(T, E, k, S);
+  if (st != MOE_OK) return st;
+  if ((topk_weights == nullptr) != (grad_weights == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!grad_loss && !grad_weights) return MOE_ERR_INVALID_ARG;
+  if (!seq_offsets && S != 1) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!grad_scores || (grad_loss && (!scores || !counts || !tokens)) || (grad_weights && !topk_ids))
+    return MOE_ERR_INVALID_ARG;
+  return from_hip(moe::launch_router_backward(scores, topk_ids, topk_weights, grad_weights,
+                                              token_mask, seq_offsets, counts, tokens, grad_loss, T,
+                                              E, k, S, grad_scores, as_stream(stream)));
+}
+
+// ---- norms around a block -------------------------------------------------
+
+moe_status moe_block_norm(const moe_block* B, void* out, void* n, void* stream) {
+  const moe_status st = check_block(B);
+  if (st != MOE_OK) return st;
+  if (B->T == 0) return MOE_OK;
+  if (!B->x || (B->y == nullptr) != (out == nullptr) || (B->w_next == nullptr) != (n == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!out && !n) return MOE_ERR_INVALID_ARG;
+  if (out == B->x && B->x_stride != B->H) return MOE_ERR_INVALID_ARG;
+  return from_hip(moe::launch_block_norm(*B, out, n, as_stream(stream)));
+}
+
+size_t moe_block_norm_backward_workspace_bytes(int32_t T, int32_t H) {
+  if (T < 0 || H < 1 || H > kMaxNormH) return 0;
+  return moe::block_norm_backward_workspace(T, H);
+}
+
+moe_status moe_block_norm_backward(const moe_block* B, const void* grad_out, const void* grad_n,
+                                   void* grad_x, void* grad_y, void* grad_gate,
+                                   float* grad_w_post, float* grad_w_next, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  const moe_status st = check_block(B);
+  if (st != MOE_OK) return st;
+  if (B->T > 0 && !B->y && !B->w_next) return MOE_ERR_INVALID_ARG;
+  if ((B->w_post == nullptr) != (grad_w_post == nullptr) ||
+      (B->w_next == nullptr) != (grad_w_next == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  const bool gated = B->gate_kind != MOE_GATE_NONE;
+  if (B->T > 0) {
+    if (!grad_x || (B->y == nullptr) != (grad_y == nullptr) || gated != (grad_gate != nullptr))
+      return MOE_ERR_INVALID_ARG;
+    if ((B->w_next != nullptr) != (grad_n != nullptr) || (B->w_next && !B->x))
+      return MOE_ERR_INVALID_ARG;
+    if (!grad_out && !grad_n) return MOE_ERR_INVALID_ARG;
+    if (!workspace) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < moe::block_norm_backward_workspace(B->T, B->H))
+      return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned16(workspace)) return MOE_ERR_INVALID_ARG;
+  } else if (B->gate_kind == MOE_GATE_CHANNEL && !grad_gate) {
+    return MOE_ERR_INVALID_ARG;
+  }
+  return from_hip(moe::launch_block_norm_backward(*B, grad_out, grad_n, grad_x, grad_y, grad_gate,
+                                                  grad_w_post, grad_w_next,
+                                                  reinterpret_cast<float*>(workspace),
+                                                  as_stream(stream)));
 }
 
 int32_t moe_choose_path(const moe_weights* W, int32_t T, int32_t k) {

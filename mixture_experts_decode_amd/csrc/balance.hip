@@ -1,0 +1,513 @@
+// Router statistics and losses, and the router's gradient.
+//
+// For every sequence s with the n_s counting tokens t, p_t = softmax(scores_t):
+//   c_se = routed slots of expert e,   f_se = E c_se / (k n_s)
+//   P_se = mean_t p_te,   L_s = sum_e f_se P_se,   Z_s = mean_t lse(scores_t)^2
+// and, c held constant (it is a count),
+//   d scores_te = p_te / n_s (gL_s (f_se - <f_s, p_t>) + 2 gZ_s lse_t)
+//                 + sum_{j: id_tj = e} w_tj (dw_tj - <w_t, dw_t>)
+// the last term being the softmax over the selected scores (moe_topk_route).
+//
+// A row's arithmetic is a softmax over E <= 1024 values, so a group of 16, 32
+// or 64 lanes takes a row with up to 16 values per lane: four rows per
+// wavefront at the usual E, reductions of four DPP steps, each score read
+// once.
+
+#include <algorithm>
+
+#include "internal.h"
+#include "rows.h"
+
+namespace moe {
+
+namespace {
+
+struct BalanceArgs {
+  const float* scores;
+  const int32_t* ids;
+  const uint8_t* mask;      // nullable
+  const int32_t* offsets;   // nullable: one sequence of all tokens
+  int T, E, k, S;
+  int block_rows;
+  float* part_p;            // [slots][E]
+  int32_t* part_c;          // [slots][E]
+  float* part_z;            // [slots]
+  int32_t* part_n;          // [slots]
+  int32_t* counts;          // [S][E]
+  int32_t* tokens;          // [S]
+  float* loss;              // [S][2]
+  const float* grad_loss;   // backward: [S][2] or null
+  const float *wts, *grad_wts;   // [T][k] or null
+  float* grad;              // [T][E]
+};
+
+// An id outside [0, E) is read as expert 0, as everywhere in the library.
+__device__ __forceinline__ int expert_of(int id, int E) { return (unsigned)id < (unsigned)E ? id : 0; }
+
+// Orders a wavefront's LDS accesses: its lanes exchange values through LDS
+// without a barrier.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Token bounds as the kernels read them: inside [0, T] whatever is stored.
+__device__ __forceinline__ int bound(const BalanceArgs& a, int s) {
+  if (!a.offsets) return s == 0 ? 0 : a.T;
+  return max(0, min(a.T, a.offsets[s]));
+}
+
+// The last sequence that starts at or before token t (-1: none, S: t lies
+// behind the last one).  Of sequences that start at the same token the last
+// one is the one that is not empty.
+__device__ __forceinline__ int sequence_of(const BalanceArgs& a, int t) {
+  if (!a.offsets) return 0;
+  int lo = 0, hi = a.S + 1;   // first index in [0, S + 1] whose start is past t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (bound(a, mid) > t) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo - 1;
+}
+
+// Lane `li` of a group of LPR holds PER values of a row: vectors of four
+// (VEC) or single values, strided over the group.
+template <int LPR, int PER, bool VEC>
+__device__ __forceinline__ int expert_at(int i, int li) {
+  return VEC ? ((i >> 2) * LPR + li) * 4 + (i & 3) : i * LPR + li;
+}
+
+template <int LPR, int PER, bool VEC>
+__device__ __forceinline__ void load_scores(float (&v)[PER], const BalanceArgs& a, int t, int li) {
+  const float* row = a.scores + (size_t)t * a.E;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+      const int e = expert_at<LPR, PER, true>(i, li);
+      const u32x4 w = load16(row + (e < a.E ? e : 0));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i + j] = __uint_as_float(w[j]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = expert_at<LPR, PER, false>(i, li);
+      v[i] = row[e < a.E ? e : 0];
+    }
+  }
+}
+
+// v -> exp(v - max) with columns past E cleared; returns the sum, the
+// maximum by reference (-inf if the row has no finite score).
+template <int LPR, int PER, bool VEC>
+__device__ __forceinline__ float exponentials(float (&v)[PER], float& m, int E, int li) {
+  m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (expert_at<LPR, PER, VEC>(i, li) >= E) v[i] = -INFINITY;
+    m = fmaxf(m, v[i]);
+  }
+  m = group_max<LPR>(m);
+  const float base = m == -INFINITY ? 0.0f : m;
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    v[i] = expf(v[i] - base);
+    s += v[i];
+  }
+  return group_sum<LPR>(s);
+}
+
+constexpr int kBalanceBlock = 1024;
+
+// Loss of one sequence from its column sums (p and c of expert e in LDS) and
+// its z sum and token count; every thread of the workgroup calls it.
+__device__ __forceinline__ void finish_sequence(const BalanceArgs& a, int s, const float* p,
+                                                const int32_t* c, float z, int n, float* red) {
+  float sum = 0.0f;
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+    a.counts[(size_t)s * a.E + e] = c[e];
+    sum = fmaf((float)c[e], p[e], sum);
+  }
+  sum = wave_sum(sum);
+  if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sum = 0.0f;
+    for (int q = 0; q < (int)blockDim.x / kWave; ++q) sum += red[q];
+    const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
+    a.loss[2 * (size_t)s] = sum * inv * inv * ((float)a.E / (float)a.k);
+    a.loss[2 * (size_t)s + 1] = z * inv;
+    a.tokens[s] = n;
+  }
+  __syncthreads();
+}
+
+// One workgroup takes `block_rows` consecutive tokens, the part of each
+// sequence among them on its own.  SINGLE: it takes all tokens and writes the
+// results; else it writes the partial sums of block b and sequence s to slot
+// b + s, which no other pair has, since both only grow along the tokens.
+template <int LPR, int PER, bool VEC, bool SINGLE>
+__global__ __launch_bounds__(kBalanceBlock) void balance_kernel(BalanceArgs a) {
+  constexpr int kGroups = kBalanceBlock / LPR;
+  constexpr int kWaves = kBalanceBlock / kWave;
+  __shared__ float s_p[kWaves][LPR * PER];
+  __shared__ int32_t s_c[LPR * PER];
+  __shared__ float s_z[kWaves];
+  __shared__ int32_t s_n[kWaves];
+  __shared__ float s_red[kWaves];
+  const int li = threadIdx.x % LPR, g = threadIdx.x / LPR;
+  const int wave = wave_in_block(), lane = threadIdx.x & (kWave - 1);
+  const int r0 = blockIdx.x * a.block_rows;
+  const int r1 = min(a.T, r0 + a.block_rows);
+  if constexpr (SINGLE) {
+    // sequences without a token are met by no row
+    for (int s = wave; s < a.S; s += kWaves) {
+      if (bound(a, s + 1) > bound(a, s)) continue;
+      for (int e = lane; e < a.E; e += kWave) a.counts[(size_t)s * a.E + e] = 0;
+      if (lane == 0) a.tokens[s] = 0, a.loss[2 * s] = 0.0f, a.loss[2 * s + 1] = 0.0f;
+    }
+  }
+  int r = r0;
+  while (r < r1) {
+    const int seq = sequence_of(a, r);
+    if (seq >= a.S) break;
+    if (seq < 0) {
+      r = max(r + 1, bound(a, 0));
+      continue;
+    }
+    const int end = max(r + 1, min(r1, bound(a, seq + 1)));
+    for (int e = threadIdx.x; e < LPR * PER; e += kBalanceBlock) s_c[e] = 0;
+    __syncthreads();
+    float acc[PER] = {}, z = 0.0f;
+    int n = 0;
+    for (int t = r + g; t < end; t += kGroups) {
+      if (a.mask && !a.mask[t]) continue;
+      float v[PER], m;
+      load_scores<LPR, PER, VEC>(v, a, t, li);
+      const float sum = exponentials<LPR, PER, VEC>(v, m, a.E, li);
+      if (m == -INFINITY) continue;
+      const float inv = 1.0f / sum;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+      const float lse = m + logf(sum);
+      z = fmaf(lse, lse, z);
+      ++n;
+      for (int j = li; j < a.k; j += LPR) {
+        atomicAdd(&s_c[expert_of(a.ids[(size_t)t * a.k + j], a.E)], 1);
+      }
+    }
+    // the wavefront's groups, then the wavefronts
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if constexpr (LPR == 16) acc[i] += __shfl_xor(acc[i], 16, kWave);
+      if constexpr (LPR <= 32) acc[i] += __shfl_xor(acc[i], 32, kWave);
+      if (lane < LPR) s_p[wave][expert_at<LPR, PER, VEC>(i, li)] = acc[i];
+    }
+    z = li == 0 ? z : 0.0f;
+    z = wave_sum(z);
+    n = li == 0 ? n : 0;
+    for (int off = kWave / 2; off > 0; off >>= 1) n += __shfl_xor(n, off, kWave);
+    if (lane == 0) s_z[wave] = z, s_n[wave] = n;
+    __syncthreads();
+    z = 0.0f, n = 0;
+    for (int w = 0; w < kWaves; ++w) z += s_z[w], n += s_n[w];
+    const size_t slot = (size_t)blockIdx.x + seq;
+    for (int e = threadIdx.x; e < a.E; e += kBalanceBlock) {
+      float p = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) p += s_p[w][e];
+      if constexpr (SINGLE) {
+        s_p[0][e] = p;
+      } else {
+        a.part_p[slot * a.E + e] = p;
+        a.part_c[slot * a.E + e] = s_c[e];
+      }
+    }
+    if constexpr (SINGLE) {
+      __syncthreads();
+      finish_sequence(a, seq, s_p[0], s_c, z, n, s_red);
+    } else {
+      if (threadIdx.x == 0) a.part_z[slot] = z, a.part_n[slot] = n;
+      __syncthreads();
+    }
+    r = end;
+  }
+}
+
+// One workgroup per sequence adds its slots in order.
+__global__ __launch_bounds__(kBalanceBlock) void balance_finish_kernel(BalanceArgs a) {
+  __shared__ float s_p[kBalanceBlock];
+  __shared__ int32_t s_c[kBalanceBlock];
+  __shared__ float s_red[kBalanceBlock / kWave];
+  __shared__ float s_zs[kBalanceBlock / kWave];
+  __shared__ int32_t s_ns[kBalanceBlock / kWave];
+  const int s = blockIdx.x;
+  const int first = bound(a, s), end = bound(a, s + 1);
+  const int b0 = end > first ? first / a.block_rows : 0;
+  const int b1 = end > first ? (end - 1) / a.block_rows + 1 : 0;
+  float z = 0.0f;
+  int n = 0;
+  for (int b = b0 + threadIdx.x; b < b1; b += kBalanceBlock)
+    z += a.part_z[(size_t)b + s], n += a.part_n[(size_t)b + s];
+  z = wave_sum(z);
+  for (int off = kWave / 2; off > 0; off >>= 1) n += __shfl_xor(n, off, kWave);
+  if ((threadIdx.x & (kWave - 1)) == 0) s_zs[threadIdx.x / kWave] = z, s_ns[threadIdx.x / kWave] = n;
+  // slices of the slots side by side over the experts
+  int width = 64;
+  while (width < a.E) width *= 2;
+  const int slices = kBalanceBlock / width;
+  const int e = threadIdx.x % width, q = threadIdx.x / width;
+  float p = 0.0f;
+  int c = 0;
+  if (e < a.E) {
+#pragma unroll 8
+    for (int b = b0 + q; b < b1; b += slices) {
+      p += a.part_p[((size_t)b + s) * a.E + e];
+      c += a.part_c[((size_t)b + s) * a.E + e];
+    }
+  }
+  s_p[threadIdx.x] = p;
+  s_c[threadIdx.x] = c;
+  __syncthreads();
+  if (q == 0) {
+    for (int i = 1; i < slices; ++i) p += s_p[i * width + e], c += s_c[i * width + e];
+    s_p[e] = p;
+    s_c[e] = c;
+  }
+  z = 0.0f, n = 0;
+  for (int w = 0; w < kBalanceBlock / kWave; ++w) z += s_zs[w], n += s_ns[w];
+  __syncthreads();
+  finish_sequence(a, s, s_p, s_c, z, n, s_red);
+}
+
+// The gradient of the scores.  A group keeps f of the sequence it is in.  The
+// k terms of the routing weights go to their experts through a row of LDS:
+// ids that are distinct need one store each; if two slots of the token name
+// one expert, one lane adds the terms in slot order.
+constexpr int kBackBlock = 256;
+
+template <int LPR, int PER, bool VEC>
+__global__ __launch_bounds__(kBackBlock) void router_back_kernel(BalanceArgs a) {
+  constexpr int kGroups = kBackBlock / LPR;
+  __shared__ float s_row[kGroups][LPR * PER];
+  const int li = threadIdx.x % LPR, g = threadIdx.x / LPR;
+  float* srow = s_row[g];
+  const int r0 = blockIdx.x * a.block_rows;
+  const int r1 = min(a.T, r0 + a.block_rows);
+  if (a.grad_wts) {
+    for (int e = li; e < LPR * PER; e += LPR) srow[e] = 0.0f;
+    wave_fence();
+  }
+  int seq = -2, seq_end = r0;
+  float f[PER], gl = 0.0f, gz = 0.0f;
+  for (int t = r0 + g; t < r1; t += kGroups) {
+    bool live = a.grad_loss != nullptr && !(a.mask && !a.mask[t]);
+    if (live && t >= seq_end) {
+      seq = sequence_of(a, t);
+      seq_end = seq >= a.S ? a.T : bound(a, seq + 1);
+      const int n = seq >= 0 && seq < a.S ? a.tokens[seq] : 0;
+      const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
+      gl = gz = 0.0f;
+      if (n > 0) {
+        gl = a.grad_loss[2 * (size_t)seq] * inv;
+        gz = 2.0f * a.grad_loss[2 * (size_t)seq + 1] * inv;
+      }
+      const float scale = inv * ((float)a.E / (float)a.k);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int e = expert_at<LPR, PER, VEC>(i, li);
+        f[i] = n > 0 && e < a.E ? (float)a.counts[(size_t)seq * a.E + e] * scale : 0.0f;
+      }
+    }
+    live = live && seq >= 0 && seq < a.S;
+    float d[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) d[i] = 0.0f;
+    if (live) {
+      float m;
+      load_scores<LPR, PER, VEC>(d, a, t, li);
+      const float sum = exponentials<LPR, PER, VEC>(d, m, a.E, li);
+      const float inv = m == -INFINITY ? 0.0f : 1.0f / sum;
+      float fp = 0.0f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        d[i] *= inv;
+        fp = fmaf(f[i], d[i], fp);
+      }
+      fp = group_sum<LPR>(fp);
+      const float lse = m == -INFINITY ? 0.0f : m + logf(sum);
+      const float base = fmaf(gz, lse, -(gl * fp));
+#pragma unroll
+      for (int i = 0; i < PER; ++i) d[i] *= fmaf(gl, f[i], base);
+    }
+    if (a.grad_wts) {
+      const int32_t* ids = a.ids + (size_t)t * a.k;
+      const float* w = a.wts + (size_t)t * a.k;
+      const float* dw = a.grad_wts + (size_t)t * a.k;
+      float dot = 0.0f;
+      for (int j = li; j < a.k; j += LPR) dot = fmaf(w[j], dw[j], dot);
+      dot = group_sum<LPR>(dot);
+      // every slot writes its number to its expert's place; a slot that does
+      // not find its own there shares the expert with another one
+      for (int j = li; j < a.k; j += LPR) srow[expert_of(ids[j], a.E)] = (float)j;
+      wave_fence();
+      bool alone = true;
+      for (int j = li; j < a.k; j += LPR) alone = alone && srow[expert_of(ids[j], a.E)] == (float)j;
+      wave_fence();
+      if (__ballot(!alone) == 0) {
+        for (int j = li; j < a.k; j += LPR) srow[expert_of(ids[j], a.E)] = w[j] * (dw[j] - dot);
+      } else if (li == 0) {
+        for (int j = 0; j < a.k; ++j) srow[expert_of(ids[j], a.E)] = 0.0f;
+        for (int j = 0; j < a.k; ++j) srow[expert_of(ids[j], a.E)] += w[j] * (dw[j] - dot);
+      }
+      wave_fence();
+#pragma unroll
+      for (int i = 0; i < PER; ++i) d[i] += srow[expert_at<LPR, PER, VEC>(i, li)];
+      wave_fence();
+      for (int j = li; j < a.k; j += LPR) srow[expert_of(ids[j], a.E)] = 0.0f;
+      wave_fence();
+    }
+    float* out = a.grad + (size_t)t * a.E;
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < PER; i += 4) {
+        const int e = expert_at<LPR, PER, true>(i, li);
+        if (e < a.E)
+          *reinterpret_cast<u32x4*>(out + e) =
+              u32x4{__float_as_uint(d[i]), __float_as_uint(d[i + 1]), __float_as_uint(d[i + 2]),
+                    __float_as_uint(d[i + 3])};
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int e = expert_at<LPR, PER, false>(i, li);
+        if (e < a.E) out[e] = d[i];
+      }
+    }
+  }
+}
+
+// Lanes per row by E (up to 16 values per lane).
+int lanes_of(int E) { return E <= 256 ? 16 : E <= 512 ? 32 : 64; }
+
+// Tokens per workgroup of the forward pass: whole rounds of its groups, and
+// about one workgroup per CU, whose partial sums then stay few.
+int block_rows_of(int T, int E) {
+  const int round = kBalanceBlock / lanes_of(E);
+  const int cus = device_num_cus();
+  const int rounds = std::max(1, (int)(((long long)T + (long long)round * cus - 1) / ((long long)round * cus)));
+  return rounds * round;
+}
+
+// All tokens in one workgroup and one launch: up to four rounds of its
+// groups, and few sequences, which it takes one after the other.
+bool single_block(int T, int E, int S) { return S <= 4 && T <= 4 * (kBalanceBlock / lanes_of(E)); }
+
+int blocks_of(int T, int E) {
+  const int rows = block_rows_of(T, E);
+  return (int)(((long long)T + rows - 1) / rows);
+}
+
+size_t padded(size_t v) { return (v + 255) / 256 * 256; }
+
+template <int LPR, int PER>
+void launch_forward(const BalanceArgs& a, bool vec, bool single, unsigned grid, hipStream_t s) {
+  const dim3 block(kBalanceBlock);
+  if (single) {
+    if (vec) hipLaunchKernelGGL((balance_kernel<LPR, PER, true, true>), dim3(1), block, 0, s, a);
+    else hipLaunchKernelGGL((balance_kernel<LPR, PER, false, true>), dim3(1), block, 0, s, a);
+  } else {
+    if (vec) hipLaunchKernelGGL((balance_kernel<LPR, PER, true, false>), dim3(grid), block, 0, s, a);
+    else hipLaunchKernelGGL((balance_kernel<LPR, PER, false, false>), dim3(grid), block, 0, s, a);
+  }
+}
+
+template <int LPR, int PER>
+void launch_backward(const BalanceArgs& a, bool vec, unsigned grid, hipStream_t s) {
+  if (vec) hipLaunchKernelGGL((router_back_kernel<LPR, PER, true>), dim3(grid), dim3(kBackBlock), 0, s, a);
+  else hipLaunchKernelGGL((router_back_kernel<LPR, PER, false>), dim3(grid), dim3(kBackBlock), 0, s, a);
+}
+
+}  // namespace
+
+size_t balance_workspace_bytes(int T, int E, int S) {
+  if (single_block(T, E, S)) return 0;
+  const size_t slots = (size_t)blocks_of(T, E) + S;
+  return 2 * padded(slots * E * 4) + 2 * padded(slots * 4);
+}
+
+hipError_t launch_balance(const float* scores, const int32_t* ids, const uint8_t* mask,
+                          const int32_t* offsets, int T, int E, int k, int S, int32_t* counts,
+                          int32_t* tokens, float* loss, void* ws, hipStream_t s) {
+  BalanceArgs a{};
+  a.scores = scores;
+  a.ids = ids;
+  a.mask = mask;
+  a.offsets = offsets;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.S = S;
+  a.counts = counts;
+  a.tokens = tokens;
+  a.loss = loss;
+  const bool vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(scores) & 15u) == 0;
+  const bool single = single_block(T, E, S);
+  a.block_rows = single ? std::max(T, 1) : block_rows_of(T, E);
+  const int blocks = single ? 1 : blocks_of(T, E);
+  if (!single) {
+    const size_t slots = (size_t)blocks + S;
+    char* p = reinterpret_cast<char*>(ws);
+    a.part_p = reinterpret_cast<float*>(p);
+    a.part_c = reinterpret_cast<int32_t*>(p += padded(slots * E * 4));
+    a.part_z = reinterpret_cast<float*>(p += padded(slots * E * 4));
+    a.part_n = reinterpret_cast<int32_t*>(p += padded(slots * 4));
+  }
+  if (E <= 64) launch_forward<16, 4>(a, vec, single, blocks, s);
+  else if (E <= 128) launch_forward<16, 8>(a, vec, single, blocks, s);
+  else if (E <= 256) launch_forward<16, 16>(a, vec, single, blocks, s);
+  else if (E <= 512) launch_forward<32, 16>(a, vec, single, blocks, s);
+  else launch_forward<64, 16>(a, vec, single, blocks, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || single) return e;
+  hipLaunchKernelGGL(balance_finish_kernel, dim3(S), dim3(kBalanceBlock), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_router_backward(const float* scores, const int32_t* ids, const float* wts,
+                                  const float* grad_wts, const uint8_t* mask,
+                                  const int32_t* offsets, const int32_t* counts,
+                                  const int32_t* tokens, const float* grad_loss, int T, int E,
+                                  int k, int S, float* grad, hipStream_t s) {
+  BalanceArgs a{};
+  a.scores = scores;
+  a.ids = ids;
+  a.wts = wts;
+  a.grad_wts = grad_wts;
+  a.mask = mask;
+  a.offsets = offsets;
+  a.counts = const_cast<int32_t*>(counts);
+  a.tokens = const_cast<int32_t*>(tokens);
+  a.grad_loss = grad_loss;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.S = S;
+  a.grad = grad;
+  const bool vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(scores) & 15u) == 0 &&
+                   (reinterpret_cast<uintptr_t>(grad) & 15u) == 0;
+  const int round = kBackBlock / lanes_of(E);
+  const long long most = (long long)device_num_cus() * 8 * round;
+  a.block_rows = (int)std::max(1LL, ((long long)T + most - 1) / most) * round;
+  const unsigned grid = (unsigned)(((long long)T + a.block_rows - 1) / a.block_rows);
+  if (E <= 64) launch_backward<16, 4>(a, vec, grid, s);
+  else if (E <= 128) launch_backward<16, 8>(a, vec, grid, s);
+  else if (E <= 256) launch_backward<16, 16>(a, vec, grid, s);
+  else if (E <= 512) launch_backward<32, 16>(a, vec, grid, s);
+  else launch_backward<64, 16>(a, vec, grid, s);
+  return hipGetLastError();
+}
+
+}  // namespace moe

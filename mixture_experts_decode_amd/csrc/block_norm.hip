@@ -1,0 +1,538 @@
+// Norms before and after a block, fused with its gate and residual scale.
+//
+//   b_t = y_t / rms(y_t) (.) w_post      (y_t itself without w_post)
+//   o_t = res_scale * x_t + g_t (.) b_t  (x_t itself without y)
+//   n_t = o_t / rms(o_t) (.) w_next,     rms(v) = sqrt(mean v^2 + eps)
+//
+// The arithmetic is a few operations per value read, so HBM bounds it: the
+// row is read once, kept in registers over both norms and written once.  All
+// sums and statistics are FP32; o and n are each rounded once, n from the
+// unrounded o.
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "internal.h"
+#include "rows.h"
+
+namespace moe {
+
+namespace {
+
+enum YKind { Y_NONE = 0, Y_BF16 = 1, Y_F32 = 2 };
+
+struct NormArgs {
+  int T, H, gate_kind;
+  float a, eps, inv_h;
+  long long xs, ys;                  // elements between rows
+  const void *x, *y, *wp, *wn, *gate;
+  void *out, *n;                     // forward
+  const void *go, *gn;               // backward
+  void *dx, *dy, *dgate;
+  float* part;                       // [3][parts][H] column sums
+  int parts;
+};
+
+// Eight elements per vector; thread `tid` of the NT that share a row owns
+// vectors tid, tid + NT, ... (VEC), or single elements tid, tid + NT, ...
+// where a row's start or length is no multiple of 16 bytes.
+template <int NT, bool VEC>
+__device__ __forceinline__ int column(int v, int i, int tid) {
+  return VEC ? (v * NT + tid) * 8 + i : (v * 8 + i) * NT + tid;
+}
+
+// Eight elements of a row as stored.  A thread past the row's end reads its
+// first columns instead and has them cleared by `unpack`: loads without a
+// branch of their own are all in flight before the first one is waited for.
+template <bool F32, bool VEC> struct Row {
+  Raw8<F32> raw;
+};
+template <bool F32> struct Row<F32, false> {
+  uint32_t raw[8];
+};
+
+template <bool F32, int NT, bool VEC>
+__device__ __forceinline__ Row<F32, VEC> fetch(const void* p, size_t base, int v, int tid, int H) {
+  Row<F32, VEC> r;
+  if constexpr (VEC) {
+    const int c = column<NT, true>(v, 0, tid);
+    const size_t at = base + (c < H ? c : 0);
+    if constexpr (F32) {
+      const float* q = reinterpret_cast<const float*>(p) + at;
+      r.raw.a[0] = load16(q);
+      r.raw.a[1] = load16(q + 4);
+    } else {
+      r.raw.a = load16(reinterpret_cast<const uint16_t*>(p) + at);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<NT, false>(v, i, tid);
+      const size_t at = base + (c < H ? c : 0);
+      if constexpr (F32) r.raw[i] = reinterpret_cast<const uint32_t*>(p)[at];
+      else r.raw[i] = reinterpret_cast<const uint16_t*>(p)[at];
+    }
+  }
+  return r;
+}
+
+template <bool F32, int NT, bool VEC>
+__device__ __forceinline__ void unpack(float (&f)[8], const Row<F32, VEC>& r, int v, int tid,
+                                       int H) {
+  if constexpr (VEC) {
+    const uint32_t keep = column<NT, true>(v, 0, tid) < H ? 0xffffffffu : 0u;
+    Raw8<F32> w = r.raw;
+    if constexpr (F32) w.a[0] &= keep, w.a[1] &= keep;
+    else w.a &= keep;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = w.get(i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w = column<NT, false>(v, i, tid) < H ? r.raw[i] : 0u;
+      f[i] = __uint_as_float(F32 ? w : w << 16);
+    }
+  }
+}
+
+template <bool F32, int NT, bool VEC, int V>
+__device__ __forceinline__ void fetch_all(Row<F32, VEC> (&r)[V], const void* p, size_t base, int tid,
+                                          int H) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) r[v] = fetch<F32, NT, VEC>(p, base, v, tid, H);
+}
+
+template <bool F32, int NT, bool VEC, int V>
+__device__ __forceinline__ void unpack_all(float (&f)[V][8], const Row<F32, VEC> (&r)[V], int tid,
+                                           int H) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) unpack<F32, NT, VEC>(f[v], r[v], v, tid, H);
+}
+
+template <bool F32, int NT, bool VEC>
+__device__ __forceinline__ void store_row(const float (&r)[8], void* p, size_t base, int v, int tid,
+                                          int H) {
+  if constexpr (VEC) {
+    const int c = column<NT, true>(v, 0, tid);
+    if (c < H) store8<F32>(p, base + c, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<NT, false>(v, i, tid);
+      if (c < H) store1<F32>(p, base + c, r[i]);
+    }
+  }
+}
+
+// Sums of M values over the NT threads of a row.  One barrier: the next call
+// writes the other half of `lds`, and a half is written again only after the
+// barrier of the call between.
+template <int NT, int M>
+__device__ __forceinline__ void row_sums(float (&s)[M], float* lds, int& half) {
+#pragma unroll
+  for (int m = 0; m < M; ++m) s[m] = wave_sum(s[m]);
+  if constexpr (NT > kWave) {
+    constexpr int W = NT / kWave;
+    float* p = lds + half * (W * 4);
+    const int w = wave_in_block();
+    if ((threadIdx.x & (kWave - 1)) == 0) {
+#pragma unroll
+      for (int m = 0; m < M; ++m) p[w * 4 + m] = s[m];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      s[m] = 0.0f;
+#pragma unroll
+      for (int q = 0; q < W; ++q) s[m] += p[q * 4 + m];
+    }
+    half ^= 1;
+  }
+}
+
+template <bool XF, int Y, int NT, int V, bool VEC>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_kernel(NormArgs a) {
+  constexpr int kRows = NT < 256 ? 256 / NT : 1;   // rows per workgroup
+  constexpr bool YF = Y == Y_F32;
+  __shared__ float lds[NT > kWave ? 2 * (NT / kWave) * 4 : 1];
+  const int tid = NT < 256 ? threadIdx.x % NT : threadIdx.x;
+  const bool gate_row = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL;
+  int half = 0;
+  for (long long t = (long long)blockIdx.x * kRows + (NT < 256 ? wave_in_block() : 0); t < a.T;
+       t += (long long)gridDim.x * kRows) {
+    const size_t row = (size_t)t * a.H;
+    Row<XF, VEC> xr[V], gr[V], pr[V], nr[V];
+    Row<YF, VEC> yr[V];
+    float gt = 1.0f;
+    fetch_all<XF, NT, VEC>(xr, a.x, (size_t)t * a.xs, tid, a.H);
+    if constexpr (Y != Y_NONE) {
+      fetch_all<YF, NT, VEC>(yr, a.y, (size_t)t * a.ys, tid, a.H);
+      if (gate_row)
+        fetch_all<XF, NT, VEC>(gr, a.gate, a.gate_kind == MOE_GATE_FULL ? row : 0, tid, a.H);
+      if (a.gate_kind == MOE_GATE_TOKEN) gt = reinterpret_cast<const float*>(a.gate)[t];
+      if (a.wp) fetch_all<XF, NT, VEC>(pr, a.wp, 0, tid, a.H);
+    }
+    if (a.wn) fetch_all<XF, NT, VEC>(nr, a.wn, 0, tid, a.H);
+    float o[V][8];
+    unpack_all<XF, NT, VEC>(o, xr, tid, a.H);
+    if constexpr (Y != Y_NONE) {
+      float y[V][8], w[V][8];
+      unpack_all<YF, NT, VEC>(y, yr, tid, a.H);
+      if (a.wp) {
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[0] = fmaf(y[v][i], y[v][i], s[0]);
+        row_sums<NT, 1>(s, lds, half);
+        const float r = rsqrtf(fmaf(s[0], a.inv_h, a.eps));
+        unpack_all<XF, NT, VEC>(w, pr, tid, a.H);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[v][i] = y[v][i] * r * w[v][i];
+      }
+      if (gate_row) {
+        unpack_all<XF, NT, VEC>(w, gr, tid, a.H);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[v][i] *= w[v][i];
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[v][i] = fmaf(a.a, o[v][i], y[v][i] * gt);
+        store_row<XF, NT, VEC>(o[v], a.out, row, v, tid, a.H);
+      }
+    }
+    if (a.wn) {
+      float s[1] = {0.0f}, w[V][8];
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[0] = fmaf(o[v][i], o[v][i], s[0]);
+      row_sums<NT, 1>(s, lds, half);
+      const float r = rsqrtf(fmaf(s[0], a.inv_h, a.eps));
+      unpack_all<XF, NT, VEC>(w, nr, tid, a.H);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[v][i] = o[v][i] * r * w[v][i];
+        store_row<XF, NT, VEC>(w[v], a.n, row, v, tid, a.H);
+      }
+    }
+  }
+}
+
+// The backward pass, with x the stored o:
+//   D  = do + r w_next (.) dn - o r^3/H <w_next (.) dn, o>      r = 1/rms(o)
+//   dx = res_scale D,   q = g (.) D,   dg = D (.) b
+//   dy = r w_post (.) q - y r^3/H <w_post (.) q, y>             r = 1/rms(y)
+//   dw_next = sum_t dn o r,  dw_post = sum_t q y r
+// The three sums of squares and products that D needs come from one
+// reduction over the row, the product that dy (and a token's gate) needs from
+// a second one.  A workgroup walks rows with a fixed stride and keeps its
+// columns' sums over them in registers; a second kernel adds the workgroups'
+// sums in order, so equal inputs give equal bits.
+template <bool XF, int Y, int NT, int V, bool VEC>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_back_kernel(NormArgs a) {
+  constexpr int kRows = NT < 256 ? 256 / NT : 1;
+  constexpr bool YF = Y == Y_F32;
+  __shared__ float lds[NT > kWave ? 2 * (NT / kWave) * 4 : 1];
+  const int tid = NT < 256 ? threadIdx.x % NT : threadIdx.x;
+  const int part = blockIdx.x * kRows + (NT < 256 ? wave_in_block() : 0);
+  int half = 0;
+  Row<XF, VEC> wn[V], wp[V], gc[V];
+  float swn[V][8] = {}, swp[V][8] = {}, sg[V][8] = {};
+  if (a.wn) fetch_all<XF, NT, VEC>(wn, a.wn, 0, tid, a.H);
+  if constexpr (Y != Y_NONE) {
+    if (a.wp) fetch_all<XF, NT, VEC>(wp, a.wp, 0, tid, a.H);
+    if (a.gate_kind == MOE_GATE_CHANNEL) fetch_all<XF, NT, VEC>(gc, a.gate, 0, tid, a.H);
+  }
+  for (long long t = part; t < a.T; t += a.parts) {
+    const size_t row = (size_t)t * a.H;
+    Row<XF, VEC> dr[V], orow[V], gr[V];
+    Row<YF, VEC> yr[V];
+    float gt = 1.0f;
+    if (a.go) fetch_all<XF, NT, VEC>(dr, a.go, row, tid, a.H);
+    if (a.wn) {
+      fetch_all<XF, NT, VEC>(orow, a.x, (size_t)t * a.xs, tid, a.H);
+      fetch_all<XF, NT, VEC>(gr, a.gn, row, tid, a.H);
+    }
+    if constexpr (Y != Y_NONE) {
+      fetch_all<YF, NT, VEC>(yr, a.y, (size_t)t * a.ys, tid, a.H);
+      if (a.gate_kind == MOE_GATE_FULL) fetch_all<XF, NT, VEC>(gc, a.gate, row, tid, a.H);
+      if (a.gate_kind == MOE_GATE_TOKEN) gt = reinterpret_cast<const float*>(a.gate)[t];
+    }
+    float d[V][8] = {}, y[V][8];
+    float s[3] = {0.0f, 0.0f, 0.0f};
+    if (a.go) unpack_all<XF, NT, VEC>(d, dr, tid, a.H);
+    if constexpr (Y != Y_NONE) {
+      unpack_all<YF, NT, VEC>(y, yr, tid, a.H);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[2] = fmaf(y[v][i], y[v][i], s[2]);
+    }
+    if (a.wn) {
+      float o[V][8], g[V][8], w[V][8];
+      unpack_all<XF, NT, VEC>(o, orow, tid, a.H);
+      unpack_all<XF, NT, VEC>(g, gr, tid, a.H);
+      unpack_all<XF, NT, VEC>(w, wn, tid, a.H);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s[0] = fmaf(o[v][i], o[v][i], s[0]);
+          s[1] = fmaf(w[v][i] * g[v][i], o[v][i], s[1]);
+        }
+      row_sums<NT, 3>(s, lds, half);
+      const float r = rsqrtf(fmaf(s[0], a.inv_h, a.eps));
+      const float c = r * r * r * (s[1] * a.inv_h);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          d[v][i] += fmaf(r * w[v][i], g[v][i], -(o[v][i] * c));
+          swn[v][i] = fmaf(g[v][i] * o[v][i], r, swn[v][i]);
+        }
+    } else if (Y != Y_NONE && a.wp) {
+      row_sums<NT, 3>(s, lds, half);
+    }
+    const float scale = Y != Y_NONE ? a.a : 1.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = scale * d[v][i];
+      store_row<XF, NT, VEC>(w, a.dx, row, v, tid, a.H);
+    }
+    if constexpr (Y != Y_NONE) {
+      const float ry = a.wp ? rsqrtf(fmaf(s[2], a.inv_h, a.eps)) : 1.0f;
+      const bool gate_row = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL;
+      float w[V][8], g[V][8];
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[v][i] = 1.0f, g[v][i] = gt;
+      if (a.wp) unpack_all<XF, NT, VEC>(w, wp, tid, a.H);
+      if (gate_row) unpack_all<XF, NT, VEC>(g, gc, tid, a.H);
+      // u = <q w_post, y>; a token's gate enters as a factor of it
+      float u[1] = {0.0f};
+      if (a.wp || a.gate_kind == MOE_GATE_TOKEN) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            u[0] = fmaf(d[v][i] * (gate_row ? g[v][i] : 1.0f) * w[v][i], y[v][i], u[0]);
+        row_sums<NT, 1>(u, lds, half);
+        if (a.gate_kind == MOE_GATE_TOKEN && tid == 0)
+          reinterpret_cast<float*>(a.dgate)[t] = ry * u[0];
+      }
+      const float c = a.wp ? ry * ry * ry * (gt * u[0] * a.inv_h) : 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float dg[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float q = d[v][i] * g[v][i], yn = y[v][i] * ry;
+          dg[i] = d[v][i] * (yn * w[v][i]);
+          swp[v][i] = fmaf(q, yn, swp[v][i]);
+          sg[v][i] += dg[i];
+          y[v][i] = fmaf(ry * w[v][i], q, -(y[v][i] * c));
+        }
+        if (a.gate_kind == MOE_GATE_FULL) store_row<XF, NT, VEC>(dg, a.dgate, row, v, tid, a.H);
+        store_row<YF, NT, VEC>(y[v], a.dy, row, v, tid, a.H);
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const size_t at = (size_t)part * a.H, plane = (size_t)a.parts * a.H;
+    if (a.wn) store_row<true, NT, VEC>(swn[v], a.part, at, v, tid, a.H);
+    if constexpr (Y != Y_NONE) {
+      if (a.wp) store_row<true, NT, VEC>(swp[v], a.part + plane, at, v, tid, a.H);
+      if (a.gate_kind == MOE_GATE_CHANNEL)
+        store_row<true, NT, VEC>(sg[v], a.part + 2 * plane, at, v, tid, a.H);
+    }
+  }
+}
+
+// Column sums of the workgroups' partial sums, in order: plane blockIdx.y of
+// part [3][parts][H] -> its gradient.  64 columns per workgroup, the parts
+// split over 16 wavefronts.
+constexpr int kSumWaves = 16;
+
+struct SumArgs {
+  const float* part;
+  int parts, H;
+  void* dst[3];
+};
+
+__global__ __launch_bounds__(kWave* kSumWaves) void column_sums_kernel(SumArgs a) {
+  __shared__ float lds[kSumWaves][kWave];
+  void* dst = a.dst[blockIdx.y];
+  if (!dst) return;
+  const int c = blockIdx.x * kWave + (threadIdx.x & (kWave - 1)), w = wave_in_block();
+  const float* p = a.part + (size_t)blockIdx.y * a.parts * a.H;
+  float s = 0.0f;
+  if (c < a.H) {
+#pragma unroll 4
+    for (int i = w; i < a.parts; i += kSumWaves) s += p[(size_t)i * a.H + c];
+  }
+  lds[w][threadIdx.x & (kWave - 1)] = s;
+  __syncthreads();
+  if (w == 0 && c < a.H) {
+    s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kSumWaves; ++q) s += lds[q][threadIdx.x];
+    reinterpret_cast<float*>(dst)[c] = s;
+  }
+}
+
+// A launch counts its threads in 32 bits; a workgroup of a larger batch walks
+// rows with the grid's stride.
+constexpr int kMaxGroups = 1 << 20;
+
+struct Shape {
+  int nt, v;
+};
+
+// Threads per row and vectors per thread: one vector per thread up to 8192
+// columns, so that a row's loads are all in flight at once.
+Shape shape_of(int H) {
+  if (H <= 512) return {64, 1};
+  if (H <= 2048) return {256, 1};
+  if (H <= 4096) return {512, 1};
+  if (H <= 8192) return {1024, 1};
+  return {1024, 2};
+}
+
+bool vectors_ok(const moe_block& B, std::initializer_list<const void*> rows) {
+  if (B.H % 8 || (B.T > 1 && (B.x_stride % 8 || B.y_stride % 8))) return false;
+  for (const void* p : rows)
+    if (reinterpret_cast<uintptr_t>(p) & 15u) return false;
+  return true;
+}
+
+NormArgs args_of(const moe_block& B) {
+  NormArgs a{};
+  a.T = B.T;
+  a.H = B.H;
+  a.gate_kind = B.gate_kind;
+  a.a = B.res_scale;
+  a.eps = B.eps;
+  a.inv_h = 1.0f / (float)B.H;
+  a.xs = B.x_stride;
+  a.ys = B.y_stride;
+  a.x = B.x;
+  a.y = B.y;
+  a.wp = B.w_post;
+  a.wn = B.w_next;
+  a.gate = B.gate;
+  return a;
+}
+
+template <bool BACK, bool XF, int Y, int NT, int V>
+void launch_shape(const NormArgs& a, bool vec, unsigned grid, hipStream_t s) {
+  const dim3 block(NT < 256 ? 256 : NT);
+  if constexpr (BACK) {
+    if (vec) hipLaunchKernelGGL((block_norm_back_kernel<XF, Y, NT, V, true>), dim3(grid), block, 0, s, a);
+    else hipLaunchKernelGGL((block_norm_back_kernel<XF, Y, NT, V, false>), dim3(grid), block, 0, s, a);
+  } else {
+    if (vec) hipLaunchKernelGGL((block_norm_kernel<XF, Y, NT, V, true>), dim3(grid), block, 0, s, a);
+    else hipLaunchKernelGGL((block_norm_kernel<XF, Y, NT, V, false>), dim3(grid), block, 0, s, a);
+  }
+}
+
+template <bool BACK, bool XF, int Y>
+void launch_typed(const NormArgs& a, Shape sh, bool vec, unsigned grid, hipStream_t s) {
+  switch (sh.nt * sh.v) {
+    case 64: return launch_shape<BACK, XF, Y, 64, 1>(a, vec, grid, s);
+    case 256: return launch_shape<BACK, XF, Y, 256, 1>(a, vec, grid, s);
+    case 512: return launch_shape<BACK, XF, Y, 512, 1>(a, vec, grid, s);
+    case 1024: return launch_shape<BACK, XF, Y, 1024, 1>(a, vec, grid, s);
+    default: return launch_shape<BACK, XF, Y, 1024, 2>(a, vec, grid, s);
+  }
+}
+
+template <bool BACK>
+void launch_any(const moe_block& B, const NormArgs& a, Shape sh, bool vec, unsigned grid,
+                hipStream_t s) {
+  if (B.x_dtype == MOE_DT_F32) {
+    if (B.y) launch_typed<BACK, true, Y_F32>(a, sh, vec, grid, s);
+    else launch_typed<BACK, true, Y_NONE>(a, sh, vec, grid, s);
+  } else if (!B.y) {
+    launch_typed<BACK, false, Y_NONE>(a, sh, vec, grid, s);
+  } else if (B.y_dtype == MOE_DT_F32) {
+    launch_typed<BACK, false, Y_F32>(a, sh, vec, grid, s);
+  } else {
+    launch_typed<BACK, false, Y_BF16>(a, sh, vec, grid, s);
+  }
+}
+
+int rows_per_group(Shape sh) { return sh.nt < 256 ? 256 / sh.nt : 1; }
+
+// Workgroups of the backward pass: enough to fill the CUs, few enough that
+// their partial column sums stay small next to the rows.
+int back_groups(int T, int H) {
+  const Shape sh = shape_of(H);
+  const int rows = rows_per_group(sh);
+  const int most = device_num_cus() * (sh.nt >= 512 ? 2 : 4);
+  return T > 0 ? std::min(most, (T - 1) / rows + 1) : 0;
+}
+
+}  // namespace
+
+hipError_t launch_block_norm(const moe_block& B, void* out, void* n, hipStream_t s) {
+  const Shape sh = shape_of(B.H);
+  NormArgs a = args_of(B);
+  a.out = out;
+  a.n = n;
+  const bool vec = vectors_ok(B, {B.x, B.y, B.w_post, B.w_next,
+                                  B.gate_kind == MOE_GATE_TOKEN ? nullptr : B.gate, out, n});
+  const int rows = rows_per_group(sh);
+  launch_any<false>(B, a, sh, vec, (unsigned)std::min(kMaxGroups, (B.T - 1) / rows + 1), s);
+  return hipGetLastError();
+}
+
+size_t block_norm_backward_workspace(int T, int H) {
+  return (size_t)3 * back_groups(T, H) * rows_per_group(shape_of(H)) * H * sizeof(float);
+}
+
+hipError_t launch_block_norm_backward(const moe_block& B, const void* go, const void* gn, void* dx,
+                                      void* dy, void* dgate, float* dwp, float* dwn, float* part,
+                                      hipStream_t s) {
+  const Shape sh = shape_of(B.H);
+  NormArgs a = args_of(B);
+  a.go = go;
+  a.gn = gn;
+  a.dx = dx;
+  a.dy = dy;
+  a.dgate = dgate;
+  a.part = part;
+  const int groups = back_groups(B.T, B.H);
+  a.parts = groups * rows_per_group(sh);
+  const bool token = B.gate_kind == MOE_GATE_TOKEN;
+  if (groups > 0) {
+    const bool vec = vectors_ok(B, {B.x, B.y, B.w_post, B.w_next, token ? nullptr : B.gate, go, gn,
+                                    dx, dy, token ? nullptr : dgate, part});
+    launch_any<true>(B, a, sh, vec, (unsigned)groups, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  SumArgs r{};
+  r.part = part;
+  r.parts = a.parts;
+  r.H = B.H;
+  r.dst[0] = dwn;
+  r.dst[1] = dwp;
+  r.dst[2] = B.gate_kind == MOE_GATE_CHANNEL ? dgate : nullptr;
+  if (dwn || dwp || r.dst[2])
+    hipLaunchKernelGGL(column_sums_kernel, dim3((B.H + kWave - 1) / kWave, 3),
+                       dim3(kWave * kSumWaves), 0, s, r);
+  return hipGetLastError();
+}
+
+}  // namespace moe

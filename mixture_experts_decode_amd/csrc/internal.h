@@ -68,6 +68,24 @@ hipError_t launch_check_routing(const int32_t* ids, int n, int E, int32_t* out, 
 hipError_t launch_combine(const void* slot_out, int slot_dtype, int T, int slots, int H, void* y,
                           int y_dtype, hipStream_t s);
 
+// block_norm.hip
+hipError_t launch_block_norm(const moe_block& B, void* out, void* n, hipStream_t s);
+size_t block_norm_backward_workspace(int T, int H);
+hipError_t launch_block_norm_backward(const moe_block& B, const void* go, const void* gn, void* dx,
+                                      void* dy, void* dgate, float* dwp, float* dwn, float* part,
+                                      hipStream_t s);
+
+// balance.hip
+size_t balance_workspace_bytes(int T, int E, int S);
+hipError_t launch_balance(const float* scores, const int32_t* ids, const uint8_t* mask,
+                          const int32_t* offsets, int T, int E, int k, int S, int32_t* counts,
+                          int32_t* tokens, float* loss, void* ws, hipStream_t s);
+hipError_t launch_router_backward(const float* scores, const int32_t* ids, const float* wts,
+                                  const float* grad_wts, const uint8_t* mask,
+                                  const int32_t* offsets, const int32_t* counts,
+                                  const int32_t* tokens, const float* grad_loss, int T, int E,
+                                  int k, int S, float* grad, hipStream_t s);
+
 // util.hip
 hipError_t launch_copy(const void* src, void* dst, size_t bytes, hipStream_t s);
 hipError_t launch_read(const void* src, size_t bytes, float* sink, hipStream_t s);
