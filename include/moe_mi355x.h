@@ -484,6 +484,45 @@ moe_status moe_block_norm_backward(const moe_block* B, const void* grad_out, con
                                    size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------ */
+/* Products with 4-bit weights and group scales.                        */
+/* ------------------------------------------------------------------ */
+
+/* One or more matrices of 4-bit codes.  A host struct of device pointers. */
+typedef struct {
+  int32_t rows;        /* N, outputs                                              */
+  int32_t cols;        /* K, inputs: a multiple of group                          */
+  int32_t num_mats;    /* E, matrices (experts); 1 for a dense product            */
+  int32_t group;       /* G, inputs that share a scale: a power of two, >= 32     */
+  int32_t scale_dtype; /* MOE_DT_F32 or MOE_DT_BF16                               */
+  const void* q;       /* [E][N][K/2] bytes: two codes 0..15, even input in the
+                          low nibble; 16-byte aligned                             */
+  const void* scale;   /* [E][N][K/G], finite                                     */
+  const uint8_t* zero; /* [E][N][K/G] zero points, or NULL: 8 everywhere          */
+} moe_w4_weights;
+
+/*
+ * moe_w4_linear: weight (n, i) of matrix e stands for
+ * scale[e][n][i / G] * (code[e][n][i] - zero[e][n][i / G]); the products are
+ *   topk_ids NULL (E = 1, k = 1):   y[t]    = W x[t]
+ *   topk_ids [T][k]:                y[t][j] = W[e_tj] x[t]     (x_per_slot 0)
+ *                                   y[t][j] = W[e_tj] x[t][j]  (x_per_slot 1)
+ * With swiglu the first N/2 outputs g and the last N/2 u become the N/2 outputs
+ * SiLU(g) u, and with topk_weights [T][k] every output of slot (t, j) is
+ * multiplied by its weight: two calls and moe_combine are an FFN of 4-bit
+ * experts.
+ *   x  device BF16 [T][K] or [T][k][K], 16-byte aligned
+ *   y  device [T][N'] or [T][k][N'], N' = N or N/2, y_dtype, rounded once
+ * The products code * x are exact, the sums FP32, in an order that depends on
+ * the sizes only, not on which tokens share an expert.
+ * T == 0 is a no-op.  An id outside [0, E) is read as matrix 0.  Limits
+ * (MOE_ERR_UNSUPPORTED): N <= 2^24, K <= 2^20, E <= 1024, T <= 2^21 and, with
+ * ids, T*k <= moe_decode_max_entries().
+ */
+moe_status moe_w4_linear(const moe_w4_weights* W, const uint16_t* x, const int32_t* topk_ids,
+                         const float* topk_weights, int32_t T, int32_t k, int32_t x_per_slot,
+                         int32_t swiglu, void* y, int32_t y_dtype, void* stream);
+
+/* ------------------------------------------------------------------ */
 /* The whole layer.                                                     */
 /* ------------------------------------------------------------------ */
 

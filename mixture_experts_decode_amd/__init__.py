@@ -52,6 +52,13 @@ class _Block(ctypes.Structure):
                 ("gate", ctypes.c_void_p)]
 
 
+class _W4(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("num_mats", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _Z = ctypes.c_size_t
@@ -80,6 +87,7 @@ _SIGS = {
     "moe_block_norm": (_I, [_BP, _P, _P, _P]),
     "moe_block_norm_backward_workspace_bytes": (_Z, [_I, _I]),
     "moe_block_norm_backward": (_I, [_BP, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "moe_w4_linear": (_I, [ctypes.POINTER(_W4), _P, _P, _P, _I, _I, _I, _I, _P, _I, _P]),
     "moe_choose_path": (_I, [_WP, _I, _I]),
     "moe_layer_workspace_bytes": (_Z, [_WP, _I, _I, _I, _I]),
     "moe_layer": (_I, [_WP, _P, _I, _P, _P, _I, _I, _P, _I, _I, _I, _P, _Z,
@@ -545,6 +553,64 @@ def _block_norm_backward(like, grad_out, grad_n, out, y, w_post, w_next, gate, r
         ws.data_ptr(), wsb, torch.cuda.current_stream().cuda_stream)
     _check(st, "moe_block_norm_backward")
     return g
+
+
+class W4Weights:
+    """Matrices of 4-bit codes resident on the device (see moe_w4_linear): q
+    [N][K/2] or [E][N][K/2] uint8, two codes a byte, the even input in the low
+    nibble; scale [..][N][K/G] float32 or bfloat16; zero uint8 of scale's shape,
+    or None (8)."""
+
+    def __init__(self, q, scale, zero=None):
+        _need(q.dim() in (2, 3) and scale.dim() == q.dim() and scale.dtype in _ROWS,
+              "q [E][N][K/2] and scale [E][N][K/G] float32 or bfloat16 are needed")
+        cols, groups = 2 * q.shape[-1], scale.shape[-1]
+        _need(groups > 0 and cols % groups == 0 and scale.shape[:-1] == q.shape[:-1],
+              "scale: q's shape with one value for every G inputs")
+        self.mats, (self.rows, self.cols) = (q.shape[0] if q.dim() == 3 else 1), (q.shape[-2], cols)
+        self.device = q.device
+        self.tensors = (q, scale, zero)
+        self._s = _W4(self.rows, cols, self.mats, cols // groups, _ROWS[scale.dtype],
+                      _tensor(q, "q", q, q.shape, (torch.uint8,)),
+                      _tensor(scale, "scale", q, scale.shape, (scale.dtype,)),
+                      _tensor(zero, "zero", q, scale.shape, (torch.uint8,)))
+
+    def nbytes(self):
+        return sum(t.numel() * t.element_size() for t in self.tensors if t is not None)
+
+
+def w4_linear(W, x, ids=None, weights=None, swiglu=False, y=None, y_dtype="f32", stream=None):
+    """y [T][N] = x [T][K] times the transpose of W4Weights W's one matrix; with ids
+    [T][k]: y [T][k][N] of the routed matrices, x [T][K] or [T][k][K].  swiglu:
+    SiLU(first half) * second half of the outputs; weights [T][k] float32: slot
+    (t, j)'s outputs times its weight."""
+    return _w4_linear(x, W, ids, weights, swiglu, y, y_dtype, stream=stream)
+
+
+@_on_device
+def _w4_linear(x, W, ids, weights, swiglu, y, y_dtype):
+    load()
+    _need(W.device == x.device, "W and x: on one device")
+    t = x.shape[0]
+    outs = W.rows // 2 if swiglu else W.rows
+    slots = x.dim() == 3
+    if ids is None:
+        _need(W.mats == 1, "ids are needed to choose among several matrices")
+        k, shape = 1, (t, outs)
+        _need(not slots, "x [T][K] is needed without ids")
+    else:
+        _need(ids.dim() == 2, "ids [T][k] are needed")
+        k = ids.shape[1]
+        shape = (t, k, outs)
+    if y is None:
+        y = _alloc(shape, y_dtype, x.device)
+    st = _lib.moe_w4_linear(
+        W._s, _tensor(x, "x", x, (t, k, W.cols) if slots else (t, W.cols), (torch.bfloat16,)),
+        _tensor(ids, "ids", x, (t, k), _I32), _tensor(weights, "weights", x, (t, k), _F32), t, k,
+        int(slots), int(swiglu), _tensor(y, "y", x, shape, tuple(_ROWS)), _ROWS[y.dtype],
+        torch.cuda.current_stream().cuda_stream)
+    _check(st, "moe_w4_linear")
+    return y
 
 
 def choose_path(W, t, k):

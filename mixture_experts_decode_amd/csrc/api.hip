@@ -193,6 +193,9 @@ size_t decode_workspace(const moe_weights* W, int32_t T, int32_t k) {
 constexpr int32_t kMaxNormH = 16384;        // a row's registers over one workgroup
 constexpr int32_t kMaxBalanceTokens = 1 << 30;
 constexpr int32_t kMaxSequences = 1 << 20;
+constexpr int32_t kMaxW4Rows = 1 << 24;
+constexpr int32_t kMaxW4Cols = 1 << 20;
+constexpr int32_t kMaxW4Tokens = 1 << 21;
 
 moe_status check_balance_sizes(int32_t T, int32_t E, int32_t k, int32_t S) {
   if (T < 0 || E < 1 || E > kMaxExpertsTotal || k < 1 || k > E || k > 64 || S < 1)
@@ -527,6 +530,28 @@ moe_status moe_block_norm_backward(const moe_block* B, const void* grad_out, con
                                                   grad_w_post, grad_w_next,
                                                   reinterpret_cast<float*>(workspace),
                                                   as_stream(stream)));
+}
+
+// ---- products with 4-bit weights -------------------------------------------
+
+moe_status moe_w4_linear(const moe_w4_weights* W, const uint16_t* x, const int32_t* topk_ids,
+                         const float* topk_weights, int32_t T, int32_t k, int32_t x_per_slot,
+                         int32_t swiglu, void* y, int32_t y_dtype, void* stream) {
+  if (!W || W->rows < 1 || W->cols < 1 || W->num_mats < 1 || W->group < 1 || T < 0 || k < 1)
+    return MOE_ERR_INVALID_ARG;
+  if (!dtype_ok(W->scale_dtype) || !dtype_ok(y_dtype)) return MOE_ERR_INVALID_ARG;
+  if ((x_per_slot & ~1) || (swiglu & ~1)) return MOE_ERR_INVALID_ARG;
+  if (W->group < 32 || (W->group & (W->group - 1)) || W->cols % W->group) return MOE_ERR_UNSUPPORTED;
+  if (swiglu && W->rows % 2) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!topk_ids && (W->num_mats != 1 || k != 1 || x_per_slot || topk_weights))
+    return MOE_ERR_INVALID_ARG;
+  if (!W->q || !W->scale || !x || !y || !aligned16(W->q) || !aligned16(x)) return MOE_ERR_INVALID_ARG;
+  if (W->rows > kMaxW4Rows || W->cols > kMaxW4Cols || W->num_mats > kMaxExpertsTotal ||
+      T > kMaxW4Tokens || (topk_ids && (int64_t)T * k > kDecodeMaxEntries))
+    return MOE_ERR_UNSUPPORTED;
+  return from_hip(moe::launch_w4_linear(*W, x, topk_ids, topk_weights, T, k, x_per_slot, swiglu, y,
+                                        y_dtype, as_stream(stream)));
 }
 
 int32_t moe_choose_path(const moe_weights* W, int32_t T, int32_t k) {

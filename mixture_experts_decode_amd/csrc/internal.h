@@ -86,6 +86,11 @@ hipError_t launch_router_backward(const float* scores, const int32_t* ids, const
                                   const int32_t* tokens, const float* grad_loss, int T, int E,
                                   int k, int S, float* grad, hipStream_t s);
 
+// w4.hip
+hipError_t launch_w4_linear(const moe_w4_weights& W, const uint16_t* x, const int32_t* ids,
+                            const float* wts, int T, int k, int x_per_slot, int swiglu, void* y,
+                            int y_dtype, hipStream_t s);
+
 // util.hip
 hipError_t launch_copy(const void* src, void* dst, size_t bytes, hipStream_t s);
 hipError_t launch_read(const void* src, size_t bytes, float* sink, hipStream_t s);

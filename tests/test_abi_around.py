@@ -127,3 +127,23 @@ def test_binding_refuses_host_tensors(moe):
         moe.balance_loss(torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int32))
     with pytest.raises(ValueError):
         moe.router_backward(torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int32))
+
+
+def w4(moe, T=4, k=1, ids=None, wts=None, x=DUMMY, slots=0, swiglu=0, y=DUMMY, ydt=0, **kw):
+    d = dict(rows=32, cols=128, num_mats=1, group=64, scale_dtype=1, q=4096, scale=4096, zero=None)
+    d.update(kw)
+    return moe.load().moe_w4_linear(moe._W4(**d), x, ids, wts, T, k, slots, swiglu, y, ydt, None)
+
+
+def test_w4_linear_refusals(moe):
+    assert moe.load().moe_w4_linear(None, DUMMY, None, None, 1, 1, 0, 0, DUMMY, 0, None) == moe.ERR_INVALID_ARG
+    for kw in (dict(rows=0), dict(cols=0), dict(num_mats=0), dict(group=0), dict(T=-1), dict(k=0),
+               dict(scale_dtype=3), dict(ydt=2), dict(slots=2), dict(swiglu=-1), dict(rows=31, swiglu=1),
+               dict(num_mats=2), dict(k=2), dict(slots=1), dict(wts=DUMMY), dict(q=None), dict(q=4104),
+               dict(scale=None), dict(x=None), dict(x=P(4100)), dict(y=None)):
+        assert w4(moe, **kw) == moe.ERR_INVALID_ARG, kw
+    for kw in (dict(group=16), dict(group=48, cols=96), dict(cols=96), dict(rows=(1 << 24) + 1),
+               dict(cols=1 << 21), dict(num_mats=1025, ids=DUMMY), dict(T=(1 << 21) + 1),
+               dict(T=1025, k=2, ids=DUMMY, num_mats=4)):
+        assert w4(moe, **kw) == moe.ERR_UNSUPPORTED, kw
+    assert w4(moe, T=0, x=None, y=None) == moe.OK
