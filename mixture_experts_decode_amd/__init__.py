@@ -358,16 +358,23 @@ def _on_device(fn):
     with that stream made torch's current one (as _on_stream)."""
     @functools.wraps(fn)
     def wrapped(first, *args, stream=None, **kwargs):
-        dev = first.device
-        if dev.type != "cuda":
-            raise ValueError(f"{fn.__name__}: tensors must be on a GPU, not on {dev}")
-        if stream is None and dev.index == torch.cuda.current_device():
+        dev = first.get_device()
+        if dev < 0:
+            raise ValueError(f"{fn.__name__}: tensors must be on a GPU, not on {first.device}")
+        if stream is None and dev == torch.cuda.current_device():
             return fn(first, *args, **kwargs)
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"{fn.__name__}: the stream belongs to {stream.device}, the tensors to {dev}")
+        if stream is not None and stream.device != first.device:
+            raise ValueError(f"{fn.__name__}: the stream belongs to {stream.device}, the tensors to "
+                             f"{first.device}")
         with torch.cuda.device(dev), torch.cuda.stream(stream):
             return fn(first, *args, **kwargs)
     return wrapped
+
+
+def _current(t):
+    """Handle of torch's current stream on t's device (a stream object costs
+    a small call more than its launch)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _need(cond, what):
@@ -411,14 +418,12 @@ def balance_loss(scores, ids, mask=None, seq_offsets=None):
     s, offs = _sequences(seq_offsets, scores)
     args = (_tensor(scores, "scores", scores, (t, e), _F32), _tensor(ids, "ids", scores, (t, k), _I32),
             _tensor(mask, "mask", scores, (t,), _BYTES), offs)
-    loss = torch.empty((s, 2), dtype=torch.float32, device=scores.device)
-    counts = torch.empty((s, e), dtype=torch.int32, device=scores.device)
-    tokens = torch.empty((s,), dtype=torch.int32, device=scores.device)
+    loss, counts, tokens = scores.new_empty((s, 2)), ids.new_empty((s, e)), ids.new_empty((s,))
     wsb = _lib.moe_balance_workspace_bytes(t, e, s)
     ws = torch.empty(wsb, dtype=torch.uint8, device=scores.device) if wsb else None
     st = _lib.moe_balance_loss(*args, t, e, k, s, counts.data_ptr(), tokens.data_ptr(),
                                loss.data_ptr(), None if ws is None else ws.data_ptr(), wsb,
-                               torch.cuda.current_stream().cuda_stream)
+                               _current(scores))
     _check(st, "moe_balance_loss")
     return loss, counts, tokens
 
@@ -434,16 +439,18 @@ def router_backward(scores, ids, grad_loss=None, counts=None, tokens=None, mask=
     t, e = scores.shape
     k = ids.shape[1]
     s, offs = _sequences(seq_offsets, scores)
+    po = _tensor(out, "out", scores, (t, e), _F32)
     if out is None:
-        out = torch.empty((t, e), dtype=torch.float32, device=scores.device)
+        out = torch.empty_like(scores)
+        po = out.data_ptr()
     st = _lib.moe_router_backward(
         _tensor(scores, "scores", scores, (t, e), _F32), _tensor(ids, "ids", scores, (t, k), _I32),
         _tensor(weights, "weights", scores, (t, k), _F32),
         _tensor(grad_weights, "grad_weights", scores, (t, k), _F32),
         _tensor(mask, "mask", scores, (t,), _BYTES), offs,
         _tensor(counts, "counts", scores, (s, e), _I32), _tensor(tokens, "tokens", scores, (s,), _I32),
-        _tensor(grad_loss, "grad_loss", scores, (s, 2), _F32), t, e, k, s,
-        _tensor(out, "out", scores, (t, e), _F32), torch.cuda.current_stream().cuda_stream)
+        _tensor(grad_loss, "grad_loss", scores, (s, 2), _F32), t, e, k, s, po,
+        _current(scores))
     _check(st, "moe_router_backward")
     return out
 
@@ -452,37 +459,44 @@ _ROWS = {torch.bfloat16: DT["bf16"], torch.float32: DT["f32"]}
 
 
 def _row_stride(x, name):
+    """Elements from a row of x [T][H] to the next, after its checks."""
     if x.dtype not in _ROWS:
         raise ValueError(f"{name}: bfloat16 or float32 rows are needed, not {x.dtype}")
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1) or \
-            (x.shape[0] > 1 and x.stride(0) < x.shape[1]):
+    if x.dim() != 2:
+        raise ValueError(f"{name}: rows [T][H] are needed")
+    t, h = x.shape
+    if x.is_contiguous():
+        return h
+    row, col = x.stride()
+    if (h > 1 and col != 1) or (t > 1 and row < h):
         raise ValueError(f"{name}: rows [T][H] with consecutive elements are needed")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    return row if t > 1 else h
 
 
 def _block(like, x, y, w_post, w_next, gate, res_scale, eps):
     t, h = like.shape
-    dts = (like.dtype,)
-    b = _Block()
-    b.T, b.H, b.x_dtype, b.y_dtype = t, h, _ROWS[like.dtype], _ROWS[like.dtype]
-    b.x_stride = b.y_stride = h
-    b.res_scale, b.eps = res_scale, eps
+    dt = like.dtype
+    dts, code = (dt,), _ROWS[dt]
+    px = py = pg = None
+    xs = ys = h
+    ycode, kind = code, "none"
     if x is not None:
-        b.x, b.x_stride = x.data_ptr(), _row_stride(x, "x")
+        px, xs = x.data_ptr(), _row_stride(x, "x")
     if y is not None:
-        b.y_stride = _row_stride(y, "y")
+        ys = _row_stride(y, "y")
         _need(y.shape == like.shape and y.device == like.device, "y: of x's shape and device")
-        b.y, b.y_dtype = y.data_ptr(), _ROWS[y.dtype]
-    b.w_post = _tensor(w_post, "w_post", like, (h,), dts)
-    b.w_next = _tensor(w_next, "w_next", like, (h,), dts)
-    kind = "none"
+        py, ycode = y.data_ptr(), _ROWS[y.dtype]
     if gate is not None:
-        kind = "channel" if gate.dim() == 1 else "token" if gate.shape[1] == 1 and (
-            h > 1 or gate.dtype == torch.float32) else "full"
-        shape = {"channel": (h,), "token": (t, 1), "full": (t, h)}[kind]
-        b.gate = _tensor(gate, f"gate ({kind})", like, shape, _F32 if kind == "token" else dts)
-    b.gate_kind = GATE[kind]
-    return b, kind
+        if gate.dim() == 1:
+            kind, shape, gdt = "channel", (h,), dts
+        elif gate.dim() == 2 and gate.shape[1] == 1 and (h > 1 or gate.dtype == torch.float32):
+            kind, shape, gdt = "token", (t, 1), _F32
+        else:
+            kind, shape, gdt = "full", (t, h), dts
+        pg = _tensor(gate, "gate", like, shape, gdt)
+    return _Block(t, h, code, ycode, GATE[kind], res_scale, eps, xs, ys, px, py,
+                  _tensor(w_post, "w_post", like, (h,), dts), _tensor(w_next, "w_next", like, (h,), dts),
+                  pg), kind
 
 
 @_on_device
@@ -494,19 +508,24 @@ def block_norm(x, y=None, w_post=None, w_next=None, gate=None, res_scale=1.0, ep
     any row stride; weights [H] and gate [H] (channels) or [T][H] in x's dtype,
     or gate [T][1] float32 (tokens).  out may be x (in place)."""
     load()
-    _row_stride(x, "x")
+    _need(x.dim() == 2 and x.dtype in _ROWS, "x: bfloat16 or float32 rows [T][H] are needed")
     b, _ = _block(x, x, y, w_post, w_next, gate, res_scale, eps)
+    po = pn = None
     if y is None:
         _need(out is None, "out goes with y")
     elif out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        po = out.data_ptr()
+    else:
+        po = _tensor(out, "out", x, x.shape, (x.dtype,))
     if w_next is None:
         _need(n is None, "n goes with w_next")
     elif n is None:
-        n = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dts = (x.dtype,)
-    st = _lib.moe_block_norm(b, _tensor(out, "out", x, x.shape, dts), _tensor(n, "n", x, x.shape, dts),
-                             torch.cuda.current_stream().cuda_stream)
+        n = torch.empty_like(x, memory_format=torch.contiguous_format)
+        pn = n.data_ptr()
+    else:
+        pn = _tensor(n, "n", x, x.shape, (x.dtype,))
+    st = _lib.moe_block_norm(b, po, pn, _current(x))
     _check(st, "moe_block_norm")
     return out, n
 
@@ -550,7 +569,7 @@ def _block_norm_backward(like, grad_out, grad_n, out, y, w_post, w_next, gate, r
     st = _lib.moe_block_norm_backward(
         b, _tensor(grad_out, "grad_out", like, (t, h), dts), _tensor(grad_n, "grad_n", like, (t, h), dts),
         g["x"].data_ptr(), _ptr(g["y"]), _ptr(g["gate"]), _ptr(g["w_post"]), _ptr(g["w_next"]),
-        ws.data_ptr(), wsb, torch.cuda.current_stream().cuda_stream)
+        ws.data_ptr(), wsb, _current(like))
     _check(st, "moe_block_norm_backward")
     return g
 
@@ -564,10 +583,11 @@ class W4Weights:
     def __init__(self, q, scale, zero=None):
         _need(q.dim() in (2, 3) and scale.dim() == q.dim() and scale.dtype in _ROWS,
               "q [E][N][K/2] and scale [E][N][K/G] float32 or bfloat16 are needed")
-        cols, groups = 2 * q.shape[-1], scale.shape[-1]
-        _need(groups > 0 and cols % groups == 0 and scale.shape[:-1] == q.shape[:-1],
+        (*mats, rows, half), (*smats, srows, groups) = q.shape, scale.shape
+        cols = 2 * half
+        _need(groups > 0 and cols % groups == 0 and (mats, rows) == (smats, srows),
               "scale: q's shape with one value for every G inputs")
-        self.mats, (self.rows, self.cols) = (q.shape[0] if q.dim() == 3 else 1), (q.shape[-2], cols)
+        self.mats, self.rows, self.cols = mats[0] if mats else 1, rows, cols
         self.device = q.device
         self.tensors = (q, scale, zero)
         self._s = _W4(self.rows, cols, self.mats, cols // groups, _ROWS[scale.dtype],
@@ -603,12 +623,14 @@ def _w4_linear(x, W, ids, weights, swiglu, y, y_dtype):
         k = ids.shape[1]
         shape = (t, k, outs)
     if y is None:
-        y = _alloc(shape, y_dtype, x.device)
+        y = x.new_empty(shape, dtype=torch.float32 if y_dtype == "f32" else torch.bfloat16)
+    else:
+        _tensor(y, "y", x, shape, tuple(_ROWS))
     st = _lib.moe_w4_linear(
         W._s, _tensor(x, "x", x, (t, k, W.cols) if slots else (t, W.cols), (torch.bfloat16,)),
         _tensor(ids, "ids", x, (t, k), _I32), _tensor(weights, "weights", x, (t, k), _F32), t, k,
-        int(slots), int(swiglu), _tensor(y, "y", x, shape, tuple(_ROWS)), _ROWS[y.dtype],
-        torch.cuda.current_stream().cuda_stream)
+        int(slots), int(swiglu), y.data_ptr(), _ROWS[y.dtype],
+        _current(x))
     _check(st, "moe_w4_linear")
     return y
 
