@@ -44,13 +44,6 @@ struct BalanceArgs {
 // An id outside [0, E) is read as expert 0, as everywhere in the library.
 __device__ __forceinline__ int expert_of(int id, int E) { return (unsigned)id < (unsigned)E ? id : 0; }
 
-// Orders a wavefront's LDS accesses: its lanes exchange values through LDS
-// without a barrier.
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // Token bounds as the kernels read them: inside [0, T] whatever is stored.
 __device__ __forceinline__ int bound(const BalanceArgs& a, int s) {
   if (!a.offsets) return s == 0 ? 0 : a.T;

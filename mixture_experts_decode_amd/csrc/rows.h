@@ -59,6 +59,13 @@ __device__ __forceinline__ void store8(void* p, size_t i, const float (&v)[8]) {
   }
 }
 
+// Orders a wavefront's LDS accesses: its lanes exchange values through LDS
+// without a barrier.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Sum and maximum over each aligned group of N lanes (16, 32 or 64); every
 // lane of the group gets it.
 template <int N>

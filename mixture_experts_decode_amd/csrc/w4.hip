@@ -15,6 +15,7 @@
 // FP8-to-BF16 conversion multiplies by 2^9.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "rows.h"
@@ -37,25 +38,10 @@ struct W4Args {
   int N, K, E, groups, group_shift;   // group_shift: log2(G / 32)
   int T, k, entries;
   int x_per_slot, swiglu, y_f32;
+  int by_expert;          // a grid row is an expert, else a touched one
 };
 
 constexpr int kW4MaxEntries = kDecodeMaxEntries;
-
-// Eight codes of one dword (element 0 in the lowest nibble) -> BF16 integers.
-__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w) {
-  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
-  const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u);   // elements 0..3
-  const uint32_t hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);   // elements 4..7
-  union {
-    bf16x2 p[4];
-    bf16x8 v;
-  } u;
-  u.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
-  u.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
-  u.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
-  u.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
-  return u.v;
-}
 
 // Lane (row n, group g) has loaded elements 32 g .. 32 g + 31 of its row;
 // afterwards its dword j holds elements 32 j + 8 g .. + 7, the ones that MFMA j
@@ -69,205 +55,377 @@ __device__ __forceinline__ u32x4 transpose4(u32x4 w) {
   return u32x4{c[0], c[1], d[0], d[1]};
 }
 
-// Weights, scales and zero points, as stored, of one 128-input step of NR row
-// tiles; they are converted where they are used, so that the loads of the
-// next step stay in flight over the current one.
-// GM: MFMAs (32 inputs each) to a scale group within the step.
-template <int NR, int GM>
-struct Step {
-  u32x4 w[NR];
-  uint32_t s[NR][4 / GM], z[NR][4 / GM];
+// The routed entries as every workgroup finds them: the experts that any entry
+// names, and one expert's entries in order.
+struct Lists {
+  unsigned touched[kMaxExpertsTotal / 32];
+  unsigned long long mask[kW4MaxEntries / kWave];
+  int16_t list[kW4MaxEntries];
 };
 
-template <int NR, int GM, bool SF, bool ZP>
-__device__ __forceinline__ void load_step(Step<NR, GM>& st, const W4Args& a, const size_t (&row)[NR],
-                                          int k0, int g) {
-  const int k = min(k0 + 32 * g, a.K - 32);
-#pragma unroll
-  for (int r = 0; r < NR; ++r)
-    st.w[r] = load_stream16(a.q + row[r] * (size_t)(a.K / 2) + k / 2);
-#pragma unroll
-  for (int r = 0; r < NR; ++r)
-#pragma unroll
-    for (int j = 0; j < 4 / GM; ++j) {
-      const int gr = min((k0 + 32 * GM * j) >> (5 + a.group_shift), a.groups - 1);
-      const size_t at = row[r] * a.groups + gr;
-      if constexpr (SF) st.s[r][j] = reinterpret_cast<const uint32_t*>(a.scale)[at];
-      else st.s[r][j] = reinterpret_cast<const uint16_t*>(a.scale)[at];
-      if constexpr (ZP) st.z[r][j] = a.zero[at];
-    }
+// Marks the experts that any entry names; returns their number.
+__device__ __forceinline__ int touched_experts(Lists& s, const W4Args& a) {
+  const int words = (a.E + 31) / 32;
+  for (int i = threadIdx.x; i < words; i += blockDim.x) s.touched[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.entries; i += blockDim.x) {
+    const int id = (unsigned)a.ids[i] < (unsigned)a.E ? a.ids[i] : 0;
+    atomicOr(&s.touched[id >> 5], 1u << (id & 31));
+  }
+  __syncthreads();
+  int n = 0;
+  for (int i = 0; i < words; ++i) n += __popc(s.touched[i]);
+  return n;
 }
 
-// MT tiles of 16 x rows, NR tiles of 16 weight rows per workgroup; its
-// wavefronts take 128-input steps in turn and add their sums through LDS.
-template <int MT, int NR, int GM, bool SF, bool ZP>
-__global__ __launch_bounds__(MT == 1 ? 1024 : MT == 2 ? 512 : 256) void w4_kernel(W4Args a) {
-  extern __shared__ float lds[];
-  __shared__ unsigned long long s_mask[kW4MaxEntries / kWave];
-  __shared__ int16_t s_list[kW4MaxEntries];
-  const int lane = threadIdx.x & (kWave - 1), wave = wave_in_block();
-  const int nw = blockDim.x / kWave;
-  const int n16 = lane & 15, g = lane >> 4;
-  const int outs = a.swiglu ? a.N / 2 : a.N;
-  const int e = a.ids ? blockIdx.y : 0;
-  int first = 0, count;
-  if (a.ids) {
-    // the entries of expert e, in order
-    const int chunks = (a.entries + kWave - 1) / kWave;
-    for (int c = wave; c < chunks; c += nw) {
-      const int i = c * kWave + lane;
-      int id = -1;
-      if (i < a.entries) id = (unsigned)a.ids[i] < (unsigned)a.E ? a.ids[i] : 0;
-      const unsigned long long m = __ballot(id == e);
-      if (lane == 0) s_mask[c] = m;
+// The want-th of them, or -1 if there are fewer.
+__device__ __forceinline__ int touched_expert(const Lists& s, const W4Args& a, int want) {
+  const int words = (a.E + 31) / 32;
+  for (int i = 0; i < words; ++i) {
+    unsigned w = s.touched[i];
+    const int c = __popc(w);
+    if (want < c) {
+      for (; want > 0; --want) w &= w - 1;
+      return 32 * i + __ffs(w) - 1;
     }
-    __syncthreads();
-    count = 0;
-    for (int c = 0; c < chunks; ++c) {
-      const unsigned long long m = s_mask[c];
-      if (c % nw == wave && ((m >> lane) & 1))
-        s_list[count + __popcll(m & ((1ull << lane) - 1))] = (int16_t)(c * kWave + lane);
-      count += __popcll(m);
-    }
-    if (count == 0) return;
-    __syncthreads();
-  } else {
-    first = blockIdx.y * (16 * MT);
-    count = min(a.T - first, 16 * MT);
+    want -= c;
   }
-  // weight rows of the tiles; with SwiGLU the first half of them are gate
-  // rows, the second the same outputs' up rows
-  constexpr int kHalf = NR == 1 ? 1 : NR / 2;
-  const int tile_rows = a.swiglu ? 16 * kHalf : 16 * NR;
-  const int r0 = blockIdx.x * tile_rows;
-  size_t row[NR];
+  return -1;
+}
+
+// Expert e's entries, in order, into s.list; returns their number.
+__device__ __forceinline__ int entries_of(Lists& s, const W4Args& a, int e) {
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_in_block(), nw = blockDim.x / kWave;
+  const int chunks = (a.entries + kWave - 1) / kWave;
+  for (int c = wave; c < chunks; c += nw) {
+    const int i = c * kWave + lane;
+    int id = -1;
+    if (i < a.entries) id = (unsigned)a.ids[i] < (unsigned)a.E ? a.ids[i] : 0;
+    const unsigned long long m = __ballot(id == e);
+    if (lane == 0) s.mask[c] = m;
+  }
+  __syncthreads();
+  int count = 0;
+  for (int c = 0; c < chunks; ++c) {
+    const unsigned long long m = s.mask[c];
+    if (c % nw == wave && ((m >> lane) & 1))
+      s.list[count + __popcll(m & ((1ull << lane) - 1))] = (int16_t)(c * kWave + lane);
+    count += __popcll(m);
+  }
+  __syncthreads();
+  return count;
+}
+
+// ---------------------------------------------------------------------------
+// Up to 16 x rows.  A wavefront takes kPart inputs of a tile of 16 weight rows,
+// once, and requests all of them together (512 bytes of each row), with the
+// part's scales, which go through its own LDS; x follows from the caches step
+// by step.  There is no loop to keep fed: many short wavefronts keep every
+// CU's loads in flight and even out by themselves.
+// ---------------------------------------------------------------------------
+
+// Waits for the wavefront's own LDS accesses and for the other wavefronts;
+// global loads stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Codes 0, 2, 4, 6 and 1, 3, 5, 7 of a dword -> BF16 integers in that order.
+__device__ __forceinline__ bf16x8 codes_even_odd(uint32_t w) {
+  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+  union {
+    bf16x2 p[4];
+    bf16x8 v;
+  } u;
+  u.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(even, 512.0f, false);
+  u.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(even, 512.0f, true);
+  u.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(odd, 512.0f, false);
+  u.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(odd, 512.0f, true);
+  return u.v;
+}
+
+// Eight x values in the order of codes_even_odd.
+__device__ __forceinline__ u32x4 even_odd(u32x4 v) {
+  return u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x05040100u), __builtin_amdgcn_perm(v[3], v[2], 0x05040100u),
+               __builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
+}
+
+// Lane i of each row of 16 gets lane i + N's value.
+template <int N>
+__device__ __forceinline__ u32x4 rotate16(u32x4 v) {
+  if constexpr (N == 0) return v;
+  else
+    return u32x4{dpp_u32<0x120 + 16 - N>(v[0]), dpp_u32<0x120 + 16 - N>(v[1]),
+                 dpp_u32<0x120 + 16 - N>(v[2]), dpp_u32<0x120 + 16 - N>(v[3])};
+}
+
+// Inputs of a wavefront's part, and wavefronts of a workgroup at most (with
+// four sets of x rows the registers are worth more than the wavefronts).
+// Dense products take parts of 256: 60 us for 40961 x 7168 and 5 x rows, 74
+// and 70 with parts of 512 and 1024.  With routed experts every workgroup
+// first lists its expert's entries, which longer parts spread over more work:
+// 57 us for the gate and up products of 32 tokens and 128 experts (1536 x 2048
+// each, top-8), 69 and 103 with parts of 512 and 256.
+__host__ __device__ constexpr int part_inputs(int sets, bool routed) { return sets == 1 && routed ? 1024 : 256; }
+__host__ __device__ constexpr int most_waves(int sets) { return sets == 4 ? 8 : 16; }
+
+// Dwords of a row of `groups` scales (or zero points) in LDS: an odd number,
+// so that 16 rows start in different banks.
+__host__ __device__ constexpr int staged_dwords(int groups, int size) { return (groups * size + 3) / 4 | 1; }
+
+// The scales (SIZE bytes each) of 16 rows over a part, `count` of them a row, a
+// power of two -> the wavefront's LDS.  DW: as dwords, else one by one.
+// kMost: pieces of a lane if there is a scale for every 32 inputs.
+template <int PART, int SIZE, bool DW>
+struct PartScales {
+  static constexpr int kMost = (16 * (PART / 32) / (DW ? 4 / SIZE : 1) + kWave - 1) / kWave;
+  uint32_t v[kMost];
+
+  // p: the tile's first row; of_row: pieces of a row, first: the part's first
+  // one; row_at(i): row i of the tile, from its first one
+  template <class RowAt>
+  __device__ __forceinline__ void load(const uint8_t* p, RowAt row_at, int of_row, int first, int log2n, int lane) {
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const bool up = a.swiglu && r >= kHalf;
-    const int n = min(r0 + 16 * (up ? r - kHalf : r) + n16, outs - 1);
-    row[r] = (size_t)e * a.N + n + (up ? outs : 0);
+    for (int i = 0; i < kMost; ++i) {
+      const int at = lane + kWave * i, r = at >> log2n;
+      if (i > 0 && (kWave * i >> log2n) >= 16) break;
+      const size_t piece = row_at(r & 15) * of_row + min(first + (at & ((1 << log2n) - 1)), of_row - 1);
+      if constexpr (DW || SIZE == 4) v[i] = reinterpret_cast<const uint32_t*>(p)[piece];
+      else if constexpr (SIZE == 2) v[i] = reinterpret_cast<const uint16_t*>(p)[piece];
+      else v[i] = p[piece];
+    }
   }
+  __device__ __forceinline__ void store(uint32_t* lds, int stride, int log2n, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const int at = lane + kWave * i, r = at >> log2n, c = at & ((1 << log2n) - 1);
+      if (i > 0 && (kWave * i >> log2n) >= 16) break;
+      if (r >= 16) continue;
+      if constexpr (DW || SIZE == 4) lds[r * stride + c] = v[i];
+      else if constexpr (SIZE == 2) reinterpret_cast<uint16_t*>(lds + r * stride)[c] = (uint16_t)v[i];
+      else reinterpret_cast<uint8_t*>(lds + r * stride)[c] = (uint8_t)v[i];
+    }
+  }
+};
+
+__device__ __forceinline__ int log2_of(int v) { return 31 - __clz(v); }
+
+// The x rows come in sets of eight.  Rows 0..7 of the A operand are their inputs
+// of one MFMA (even j), rows 8..15 those of the next one (odd j), so a load
+// serves two MFMAs.  Each of the two has its own accumulator, of which only its
+// rows are meant; a lane picks its four rows from the one that they belong to,
+// and the sums of x take one MFMA for both.  The order of a row's sums is the
+// same whatever the number of sets.
+template <int SETS, bool ROUTED, int GM, bool SF, bool ZP, bool DW>
+__global__ __launch_bounds__(most_waves(SETS) * kWave) void w4_tile_kernel(W4Args a) {
+  extern __shared__ __align__(16) uint32_t lds[];
+  __shared__ Lists s_entries;
+  constexpr int kSize = SF ? 4 : 2, kPer = DW ? 4 / kSize : 1, kPerZ = DW ? 4 : 1;
+  constexpr int kPart = part_inputs(SETS, ROUTED), kHalves = kPart / 128, kRows = 8 * SETS;
+  constexpr int kAhead = SETS == 1 ? 2 : 1;   // halves of x in flight before the current one
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_in_block(), waves = blockDim.x / kWave;
+  const int n16 = lane & 15, g = lane >> 4, odd = g >> 1;
+  const int outs = a.swiglu ? a.N / 2 : a.N;
+  const int tile_outs = a.swiglu ? 8 : 16;
+  const int shift = 5 + a.group_shift;
+  int e = 0, begin = 0, count = a.T;
+  if constexpr (ROUTED) {
+    if (a.by_expert) {
+      e = blockIdx.y;
+    } else {
+      if ((int)blockIdx.y >= touched_experts(s_entries, a)) return;
+      e = touched_expert(s_entries, a, blockIdx.y);
+    }
+    count = entries_of(s_entries, a, e);
+    if (count == 0) return;
+  } else {
+    begin = blockIdx.y * kRows;
+    count = min(a.T, begin + kRows);
+  }
+  // row i of the tile, from its first one: with SwiGLU eight gate rows and the
+  // same outputs' eight up rows
+  const int n0 = blockIdx.x * tile_outs, n_last = outs - 1 - n0;
+  const size_t row0 = (size_t)e * a.N + n0;
+  auto row_at = [&](int i) {
+    return a.swiglu ? min(i & 7, n_last) + (i >= 8 ? outs : 0) : min(i, n_last);
+  };
+  const uint8_t* q = a.q + (row0 + row_at(n16)) * (size_t)(a.K / 2) + 16 * g;
+  const uint8_t* scale0 = reinterpret_cast<const uint8_t*>(a.scale) + row0 * a.groups * kSize;
+  const uint8_t* zero0 = a.zero + row0 * a.groups;
+  // scales of a part in LDS, per wavefront
+  const int part_groups = min(kPart / 32, max(1, kPart >> shift));
+  const int s_row = staged_dwords(part_groups, kSize), z_row = staged_dwords(part_groups, 1);
+  uint32_t* scales = lds + wave * 16 * (s_row + (ZP ? z_row : 0));
+  uint32_t* zeros = scales + 16 * s_row;
+  const int s_log = log2_of(max(1, part_groups / kPer)), z_log = log2_of(max(1, part_groups / kPerZ));
+  float* sums = reinterpret_cast<float*>(lds + waves * 16 * (s_row + (ZP ? z_row : 0)));
+  const uint8_t* sl = reinterpret_cast<const uint8_t*>(scales + n16 * s_row);
+  const uint8_t* zl = reinterpret_cast<const uint8_t*>(zeros + n16 * z_row);
   const bf16x8 ones = {(__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f,
                        (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f, (__bf16)1.0f};
-  for (int tile = 0; tile < count; tile += 16 * MT) {
-    const uint16_t* xr[MT];
+  // inputs within a half that this lane holds: of load i, kLoadStep further
+  const int lane_k = GM == 4 ? 32 * g + 8 * (n16 >> 3) : 8 * g + 32 * (n16 >> 3);
+  constexpr int kLoadStep = GM == 4 ? 16 : 64;
+  for (int first = begin; first < count; first += kRows) {
+    const int rows = min(kRows, count - first);
+    const uint16_t* xp[SETS];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int i = min(tile + 16 * m + n16, count - 1);
-      int xi = first + i;
-      if (a.ids) xi = a.x_per_slot ? s_list[i] : s_list[i] / a.k;
-      xr[m] = a.x + (size_t)xi * a.K;
+    for (int m = 0; m < SETS; ++m) {
+      int xi = first + min(8 * m + (n16 & 7), rows - 1);
+      if constexpr (ROUTED) xi = a.x_per_slot ? s_entries.list[xi] : s_entries.list[xi] / a.k;
+      xp[m] = a.x + (size_t)xi * a.K + lane_k;
     }
-    f32x4 acc[MT][NR];
+    f32x4 acc[SETS];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < SETS; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // WHOLE: the part lies within K
+    auto part_of = [&](int k0, auto whole) {
+      constexpr bool WHOLE = decltype(whole)::value;
+      u32x4 w[kHalves], x[kAhead + 1][SETS][2];
+      PartScales<kPart, kSize, DW> sv;
+      PartScales<kPart, 1, DW> zv;
 #pragma unroll
-      for (int r = 0; r < NR; ++r) acc[m][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int stride = 128 * nw;
-    Step<NR, GM> cur, nxt;
-    int k0 = 128 * wave;
-    if (k0 < a.K) load_step<NR, GM, SF, ZP>(cur, a, row, k0, g);
-    for (; k0 < a.K; k0 += stride) {
-      u32x4 xv[MT][4];
+      for (int h = 0; h < kHalves; ++h)
+        w[h] = load16(WHOLE ? q + k0 / 2 + 64 * h : q + (min(k0 + 128 * h + 32 * g, a.K - 32) - 32 * g) / 2);
+      const int g0 = k0 >> shift;
+      sv.load(scale0, row_at, a.groups / kPer, g0 / kPer, s_log, lane);
+      if constexpr (ZP) zv.load(zero0, row_at, a.groups / kPerZ, g0 / kPerZ, z_log, lane);
+      auto load_x = [&](u32x4 (&v)[SETS][2], int h) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < SETS; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = min(k0 + 32 * j, a.K - 32) + 8 * g;
-          xv[m][j] = load16(xr[m] + k);
-        }
-      if (k0 + stride < a.K) load_step<NR, GM, SF, ZP>(nxt, a, row, k0 + stride, g);
-#pragma unroll
-      for (int r = 0; r < NR; ++r) cur.w[r] = transpose4(cur.w[r]);
-      f32x4 part[MT][NR], xs[MT];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j % GM == 0) {
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            xs[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int r = 0; r < NR; ++r) part[m][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int i = 0; i < 2; ++i) {
+            const int k = k0 + 128 * h + kLoadStep * i;
+            v[m][i] = load16(xp[m] + (WHOLE ? k : min(k, a.K - 8 - lane_k)));
           }
-        }
-        if (k0 + 32 * j < a.K) {
-          bf16x8 xb[MT];
+      };
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            xb[m] = __builtin_bit_cast(bf16x8, xv[m][j]);
-            xs[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[m], ones, xs[m], 0, 0, 0);
+      for (int h = 0; h < kAhead; ++h) load_x(x[h], h);
+      wave_fence();
+      sv.store(scales, s_row, s_log, lane);
+      if constexpr (ZP) zv.store(zeros, z_row, z_log, lane);
+      wave_fence();
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        __builtin_amdgcn_sched_barrier(0);   // a half's temporaries at a time
+        const int kh = k0 + 128 * h;
+        if (h + kAhead < kHalves) load_x(x[(h + kAhead) % (kAhead + 1)], h + kAhead);
+        // a group of 128 or more spans the half: each lane keeps its own 32
+        // inputs of it, x is read to match
+        const u32x4 wh = GM == 4 ? w[h] : transpose4(w[h]);
+        f32x4 part[SETS][2], xs[SETS];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bf16x8 we = codes_even_odd(wh[2 * i]), wo = codes_even_odd(wh[2 * i + 1]);
+          const uint32_t keep = WHOLE || kh + kLoadStep * i + lane_k < a.K ? 0xffffffffu : 0u;
+#pragma unroll
+          for (int m = 0; m < SETS; ++m) {
+            u32x4 v = x[h % (kAhead + 1)][m][i];
+            if constexpr (!WHOLE) v &= keep;
+            const bf16x8 xb = __builtin_bit_cast(bf16x8, even_odd(v));
+            if (i == 0 || GM < 4) part[m][0] = part[m][1] = xs[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            xs[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, ones, xs[m], 0, 0, 0);
+            part[m][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, we, part[m][0], 0, 0, 0);
+            part[m][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, wo, part[m][1], 0, 0, 0);
           }
+          if (i == 1 || GM < 4) {
+            // the group of this lane's rows: its own MFMA's if there is one
+            // for every MFMA
+            int gr = ((kh + (GM == 4 ? 0 : GM == 2 ? 64 * i : 64 * i + 32 * odd)) >> shift) - g0;
+            if constexpr (!WHOLE) gr = min(gr, a.groups - 1 - g0);
+            float f;
+            if constexpr (SF) f = reinterpret_cast<const float*>(sl)[gr];
+            else f = bf16_lo(reinterpret_cast<const uint16_t*>(sl)[gr]);
+            float z = 8.0f;
+            if constexpr (ZP) z = (float)zl[gr];
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            const bf16x8 wb = codes_to_bf16(cur.w[r][j]);
+            for (int m = 0; m < SETS; ++m)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-              part[m][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[m], wb, part[m][r], 0, 0, 0);
-          }
-        }
-        if (j % GM == GM - 1) {
-#pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            const float sc = __uint_as_float(SF ? cur.s[r][j / GM] : cur.s[r][j / GM] << 16);
-            const float zp = ZP ? (float)cur.z[r][j / GM] : 8.0f;
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                acc[m][r][i] = fmaf(sc, fmaf(-zp, xs[m][i], part[m][r][i]), acc[m][r][i]);
+              for (int p = 0; p < 4; ++p)
+                acc[m][p] = fmaf(f, fmaf(-z, xs[m][p], odd ? part[m][1][p] : part[m][0][p]), acc[m][p]);
           }
         }
       }
-      cur = nxt;
+    };
+    for (int k0 = kPart * wave; k0 < a.K; k0 += kPart * waves) {
+      if (k0 + kPart <= a.K) part_of(k0, std::true_type{});
+      else part_of(k0, std::false_type{});
     }
-    // the wavefronts' sums, added in order
+    // rows 8..15 of a set belong to the same x rows as rows 0..7
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < SETS; ++m)
 #pragma unroll
-      for (int r = 0; r < NR; ++r)
+      for (int p = 0; p < 4; ++p) acc[m][p] += __shfl_xor(acc[m][p], 32, kWave);
+    // the sums over the parts of K, added in order; wavefront w finishes the
+    // sets w, w + waves, ...
+    if (waves > 1) {
+      if (first > begin) lds_barrier();   // the last ones have been read
+      if (odd == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          lds[((wave * MT + m) * NR + r) * 256 + (4 * g + i) * 16 + n16] = acc[m][r][i];
-    __syncthreads();
-    const int out_tiles = a.swiglu ? kHalf : NR;
-    for (int o = threadIdx.x; o < MT * out_tiles * 256; o += blockDim.x) {
-      const int c = o & 15, m16 = (o >> 4) & 15, r = (o >> 8) % out_tiles, m = (o >> 8) / out_tiles;
-      const int i = tile + 16 * m + m16, n = r0 + 16 * r + c;
-      if (i >= count || n >= outs) continue;
-      float v = 0.0f, up = 0.0f;
-      for (int w = 0; w < nw; ++w) {
-        v += lds[((w * MT + m) * NR + r) * 256 + m16 * 16 + c];
-        if (a.swiglu) up += lds[((w * MT + m) * NR + r + kHalf) * 256 + m16 * 16 + c];
+        for (int m = 0; m < SETS; ++m)
+          *reinterpret_cast<f32x4*>(sums + (wave * SETS + m) * 128 + 4 * lane) = acc[m];
       }
-      if (a.swiglu) v = swiglu(v, up);
-      const int entry = a.ids ? s_list[i] : first + i;
-      if (a.wts) v *= a.wts[entry];
-      const size_t at = (size_t)entry * outs + n;
-      if (a.y_f32) reinterpret_cast<float*>(a.y)[at] = v;
-      else reinterpret_cast<__bf16*>(a.y)[at] = (__bf16)v;
+      lds_barrier();
     }
-    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < SETS; ++m) {
+      if (m % waves != wave) continue;
+      f32x4 v = acc[m];
+      if (waves > 1) {
+        v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int p = 0; p < waves; ++p)
+          v += *reinterpret_cast<const f32x4*>(sums + (p * SETS + m) * 128 + 4 * (lane & 31));
+      }
+      // output column n16 of the tile for x rows 8 m + 4 g ..
+      const int n = n0 + n16;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int i = 8 * m + 4 * g + p;
+        float r = v[p];
+        if (a.swiglu) r = swiglu(r, dpp_f32<0x128>(r));   // row_ror:8: the up row's sum
+        if (odd == 0 && i < rows && n16 < tile_outs && n < outs) {
+          const int entry = ROUTED ? s_entries.list[first + i] : first + i;
+          if (a.wts) r *= a.wts[entry];
+          const size_t to = (size_t)entry * outs + n;
+          if (a.y_f32) reinterpret_cast<float*>(a.y)[to] = r;
+          else reinterpret_cast<__bf16*>(a.y)[to] = (__bf16)r;
+        }
+      }
+    }
   }
 }
 
-template <int MT, int NR, int GM>
-void launch_scaled(const W4Args& a, bool sf, dim3 grid, int waves, hipStream_t s) {
-  const size_t lds = (size_t)waves * MT * NR * 256 * sizeof(float);
+template <int SETS, bool ROUTED, int GM, bool DW>
+void launch_scaled(const W4Args& a, bool sf, dim3 grid, int waves, size_t lds, hipStream_t s) {
   const dim3 block(waves * kWave);
   if (a.zero) {
-    if (sf) hipLaunchKernelGGL((w4_kernel<MT, NR, GM, true, true>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((w4_kernel<MT, NR, GM, false, true>), grid, block, lds, s, a);
+    if (sf) hipLaunchKernelGGL((w4_tile_kernel<SETS, ROUTED, GM, true, true, DW>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((w4_tile_kernel<SETS, ROUTED, GM, false, true, DW>), grid, block, lds, s, a);
   } else {
-    if (sf) hipLaunchKernelGGL((w4_kernel<MT, NR, GM, true, false>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((w4_kernel<MT, NR, GM, false, false>), grid, block, lds, s, a);
+    if (sf) hipLaunchKernelGGL((w4_tile_kernel<SETS, ROUTED, GM, true, false, DW>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((w4_tile_kernel<SETS, ROUTED, GM, false, false, DW>), grid, block, lds, s, a);
   }
 }
 
-template <int MT, int NR>
-void launch_grouped(const W4Args& a, bool sf, dim3 grid, int waves, hipStream_t s) {
-  if (a.group_shift == 0) launch_scaled<MT, NR, 1>(a, sf, grid, waves, s);
-  else if (a.group_shift == 1) launch_scaled<MT, NR, 2>(a, sf, grid, waves, s);
-  else launch_scaled<MT, NR, 4>(a, sf, grid, waves, s);
+template <int SETS, bool ROUTED, bool DW>
+void launch_grouped(const W4Args& a, bool sf, dim3 grid, int waves, size_t lds, hipStream_t s) {
+  if (a.group_shift == 0) launch_scaled<SETS, ROUTED, 1, DW>(a, sf, grid, waves, lds, s);
+  else if (a.group_shift == 1) launch_scaled<SETS, ROUTED, 2, DW>(a, sf, grid, waves, lds, s);
+  else launch_scaled<SETS, ROUTED, 4, DW>(a, sf, grid, waves, lds, s);
+}
+
+template <int SETS>
+void launch_sets(const W4Args& a, bool sf, bool dwords, dim3 grid, int waves, size_t lds, hipStream_t s) {
+  if (a.ids) {
+    if (dwords) launch_grouped<SETS, true, true>(a, sf, grid, waves, lds, s);
+    else launch_grouped<SETS, true, false>(a, sf, grid, waves, lds, s);
+  } else {
+    if (dwords) launch_grouped<SETS, false, true>(a, sf, grid, waves, lds, s);
+    else launch_grouped<SETS, false, false>(a, sf, grid, waves, lds, s);
+  }
 }
 
 }  // namespace
@@ -296,25 +454,27 @@ hipError_t launch_w4_linear(const moe_w4_weights& W, const uint16_t* x, const in
   a.y_f32 = y_dtype == MOE_DT_F32;
   const bool sf = W.scale_dtype == MOE_DT_F32;
   const int outs = swiglu ? a.N / 2 : a.N;
-  const int steps = (a.K + 127) / 128;
-  // x rows that one matrix meets: all of them, or the mean over the experts
-  const int rows = ids ? (a.entries + a.E - 1) / a.E : T;
-  const int mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  const int nr = swiglu || outs > 16 * 1024 ? 2 : 1;
-  const int tiles = (outs + (swiglu ? 16 : 16 * nr) - 1) / (swiglu ? 16 : 16 * nr);
-  const int most = mt == 1 ? 16 : mt == 2 ? 8 : 4;
-  int waves = 4;
-  while (waves < most && waves < steps && (long long)tiles * (ids ? a.E : 1) * waves < 4096) waves *= 2;
-  const dim3 grid(tiles, ids ? a.E : (T + 16 * mt - 1) / (16 * mt));
-  if (nr == 2) {
-    if (mt == 1) launch_grouped<1, 2>(a, sf, grid, waves, s);
-    else if (mt == 2) launch_grouped<2, 2>(a, sf, grid, waves, s);
-    else launch_grouped<4, 2>(a, sf, grid, waves, s);
-  } else {
-    if (mt == 1) launch_grouped<1, 1>(a, sf, grid, waves, s);
-    else if (mt == 2) launch_grouped<2, 1>(a, sf, grid, waves, s);
-    else launch_grouped<4, 1>(a, sf, grid, waves, s);
-  }
+  const int per = swiglu ? 8 : 16, tiles = (outs + per - 1) / per;
+  a.by_expert = a.entries >= a.E;
+  const int mats = ids ? std::min(a.E, a.entries) : 1;
+  // x rows that one matrix meets at a time: all of them, or what an expert is
+  // likely to get (one with more takes its rows in several passes)
+  const int rows = ids ? (3 * a.entries + a.E - 1) / a.E : T;
+  const int sets = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  const int inputs = part_inputs(sets, ids != nullptr);
+  const int waves = std::min(most_waves(sets), (a.K + inputs - 1) / inputs);
+  const int part = std::min(inputs / 32, std::max(1, inputs >> (5 + a.group_shift)));
+  // whole dwords of scales in a row and in a part of it
+  const bool dwords = (sf || (a.groups % 2 == 0 && part % 2 == 0)) &&
+                      (!a.zero || (a.groups % 4 == 0 && part % 4 == 0)) &&
+                      (reinterpret_cast<uintptr_t>(a.scale) & 3) == 0 &&
+                      (reinterpret_cast<uintptr_t>(a.zero) & 3) == 0;
+  const size_t lds = (size_t)waves * 64 * (staged_dwords(part, sf ? 4 : 2) + (a.zero ? staged_dwords(part, 1) : 0)) +
+                     (waves > 1 ? (size_t)waves * sets * 512 : 0);
+  const dim3 grid(tiles, ids ? mats : (T + 8 * sets - 1) / (8 * sets));
+  if (sets == 1) launch_sets<1>(a, sf, dwords, grid, waves, lds, s);
+  else if (sets == 2) launch_sets<2>(a, sf, dwords, grid, waves, lds, s);
+  else launch_sets<4>(a, sf, dwords, grid, waves, lds, s);
   return hipGetLastError();
 }
 
