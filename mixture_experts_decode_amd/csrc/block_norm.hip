@@ -109,12 +109,12 @@ __device__ __forceinline__ void unpack_all(float (&f)[V][8], const Row<F32, VEC>
   for (int v = 0; v < V; ++v) unpack<F32, NT, VEC>(f[v], r[v], v, tid, H);
 }
 
-template <bool F32, int NT, bool VEC>
+template <bool F32, int NT, bool VEC, bool PAST = false>
 __device__ __forceinline__ void store_row(const float (&r)[8], void* p, size_t base, int v, int tid,
                                           int H) {
   if constexpr (VEC) {
     const int c = column<NT, true>(v, 0, tid);
-    if (c < H) store8<F32>(p, base + c, r);
+    if (c < H) store8<F32, PAST>(p, base + c, r);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_kernel(NormArg
       for (int v = 0; v < V; ++v) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[v][i] = fmaf(a.a, o[v][i], y[v][i] * gt);
-        store_row<XF, NT, VEC>(o[v], a.out, row, v, tid, a.H);
+        store_row<XF, NT, VEC, true>(o[v], a.out, row, v, tid, a.H);
       }
     }
     if (a.wn) {
@@ -219,11 +219,15 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_kernel(NormArg
       for (int v = 0; v < V; ++v) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[v][i] = o[v][i] * r * w[v][i];
-        store_row<XF, NT, VEC>(w[v], a.n, row, v, tid, a.H);
+        store_row<XF, NT, VEC, true>(w[v], a.n, row, v, tid, a.H);
       }
     }
   }
 }
+
+// Threads of a workgroup of the backward pass: one row, or as many rows as
+// wavefronts, whose column sums then meet in 32 KB of LDS.
+__host__ __device__ constexpr int back_threads(int nt, int v) { return nt == kWave ? 1024 / v : nt; }
 
 // The backward pass, with x the stored o:
 //   D  = do + r w_next (.) dn - o r^3/H <w_next (.) dn, o>      r = 1/rms(o)
@@ -236,12 +240,12 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_kernel(NormArg
 // columns' sums over them in registers; a second kernel adds the workgroups'
 // sums in order, so equal inputs give equal bits.
 template <bool XF, int Y, int NT, int V, bool VEC>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_back_kernel(NormArgs a) {
-  constexpr int kRows = NT < 256 ? 256 / NT : 1;
+__global__ __launch_bounds__(back_threads(NT, V)) void block_norm_back_kernel(NormArgs a) {
+  constexpr int kRows = back_threads(NT, V) / NT;
   constexpr bool YF = Y == Y_F32;
   __shared__ float lds[NT > kWave ? 2 * (NT / kWave) * 4 : 1];
-  const int tid = NT < 256 ? threadIdx.x % NT : threadIdx.x;
-  const int part = blockIdx.x * kRows + (NT < 256 ? wave_in_block() : 0);
+  const int tid = NT == kWave ? threadIdx.x % NT : threadIdx.x;
+  const int sub = NT == kWave ? wave_in_block() : 0;
   int half = 0;
   Row<XF, VEC> wn[V], wp[V], gc[V];
   float swn[V][8] = {}, swp[V][8] = {}, sg[V][8] = {};
@@ -250,7 +254,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_back_kernel(No
     if (a.wp) fetch_all<XF, NT, VEC>(wp, a.wp, 0, tid, a.H);
     if (a.gate_kind == MOE_GATE_CHANNEL) fetch_all<XF, NT, VEC>(gc, a.gate, 0, tid, a.H);
   }
-  for (long long t = part; t < a.T; t += a.parts) {
+  for (long long t = (long long)blockIdx.x * kRows + sub; t < a.T; t += (long long)gridDim.x * kRows) {
     const size_t row = (size_t)t * a.H;
     Row<XF, VEC> dr[V], orow[V], gr[V];
     Row<YF, VEC> yr[V];
@@ -306,7 +310,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_back_kernel(No
       float w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = scale * d[v][i];
-      store_row<XF, NT, VEC>(w, a.dx, row, v, tid, a.H);
+      store_row<XF, NT, VEC, true>(w, a.dx, row, v, tid, a.H);
     }
     if constexpr (Y != Y_NONE) {
       const float ry = a.wp ? rsqrtf(fmaf(s[2], a.inv_h, a.eps)) : 1.0f;
@@ -343,19 +347,36 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_back_kernel(No
           y[v][i] = fmaf(ry * w[v][i], q, -(y[v][i] * c));
         }
         if (a.gate_kind == MOE_GATE_FULL) store_row<XF, NT, VEC>(dg, a.dgate, row, v, tid, a.H);
-        store_row<YF, NT, VEC>(y[v], a.dy, row, v, tid, a.H);
+        store_row<YF, NT, VEC, true>(y[v], a.dy, row, v, tid, a.H);
       }
     }
   }
+  // this workgroup's sums: one row of each plane
+  const size_t at = (size_t)blockIdx.x * a.H, plane = (size_t)a.parts * a.H;
+  auto join = [&](float (&sum)[V][8], float* dst) {
+    if constexpr (kRows == 1) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const size_t at = (size_t)part * a.H, plane = (size_t)a.parts * a.H;
-    if (a.wn) store_row<true, NT, VEC>(swn[v], a.part, at, v, tid, a.H);
-    if constexpr (Y != Y_NONE) {
-      if (a.wp) store_row<true, NT, VEC>(swp[v], a.part + plane, at, v, tid, a.H);
-      if (a.gate_kind == MOE_GATE_CHANNEL)
-        store_row<true, NT, VEC>(sg[v], a.part + 2 * plane, at, v, tid, a.H);
+      for (int v = 0; v < V; ++v) store_row<true, NT, VEC>(sum[v], dst, at, v, tid, a.H);
+    } else {
+      __shared__ float cols[kRows][NT * 8 * V];
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cols[sub][column<NT, VEC>(v, i, tid)] = sum[v][i];
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.H; c += back_threads(NT, V)) {
+        float s = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) s += cols[r][c];
+        dst[at + c] = s;
+      }
     }
+  };
+  if (a.wn) join(swn, a.part);
+  if constexpr (Y != Y_NONE) {
+    if (a.wp) join(swp, a.part + plane);
+    if (a.gate_kind == MOE_GATE_CHANNEL) join(sg, a.part + 2 * plane);
   }
 }
 
@@ -378,7 +399,7 @@ __global__ __launch_bounds__(kWave* kSumWaves) void column_sums_kernel(SumArgs a
   const float* p = a.part + (size_t)blockIdx.y * a.parts * a.H;
   float s = 0.0f;
   if (c < a.H) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = w; i < a.parts; i += kSumWaves) s += p[(size_t)i * a.H + c];
   }
   lds[w][threadIdx.x & (kWave - 1)] = s;
@@ -391,22 +412,32 @@ __global__ __launch_bounds__(kWave* kSumWaves) void column_sums_kernel(SumArgs a
   }
 }
 
-// A launch counts its threads in 32 bits; a workgroup of a larger batch walks
-// rows with the grid's stride.
+// One workgroup for each row, or for four short ones (16384 x 4096, y and a
+// channel gate: 94.9 us, with two workgroups per CU that walk the rows 92.8;
+// 16384 x 2048: 59 us and 65).  A launch counts its threads in 32 bits, so those
+// of a larger batch walk rows too.
 constexpr int kMaxGroups = 1 << 20;
 
 struct Shape {
   int nt, v;
 };
 
-// Threads per row and vectors per thread: one vector per thread up to 8192
-// columns, so that a row's loads are all in flight at once.
+// Threads per row and vectors per thread.
 Shape shape_of(int H) {
   if (H <= 512) return {64, 1};
   if (H <= 2048) return {256, 1};
-  if (H <= 4096) return {512, 1};
+  if (H <= 4096) return {256, 2};
   if (H <= 8192) return {1024, 1};
   return {1024, 2};
+}
+
+// The backward pass keeps three column sums beside the row.
+Shape back_shape_of(int H) {
+  if (H <= 512) return {64, 1};
+  if (H <= 2048) return {256, 1};
+  if (H <= 4096) return {256, 2};
+  if (H <= 8192) return {512, 2};
+  return {512, 4};
 }
 
 bool vectors_ok(const moe_block& B, std::initializer_list<const void*> rows) {
@@ -434,26 +465,39 @@ NormArgs args_of(const moe_block& B) {
   return a;
 }
 
-template <bool BACK, bool XF, int Y, int NT, int V>
-void launch_shape(const NormArgs& a, bool vec, unsigned grid, hipStream_t s) {
+template <bool XF, int Y, int NT, int V>
+void launch_forward(const NormArgs& a, bool vec, unsigned grid, hipStream_t s) {
   const dim3 block(NT < 256 ? 256 : NT);
-  if constexpr (BACK) {
-    if (vec) hipLaunchKernelGGL((block_norm_back_kernel<XF, Y, NT, V, true>), dim3(grid), block, 0, s, a);
-    else hipLaunchKernelGGL((block_norm_back_kernel<XF, Y, NT, V, false>), dim3(grid), block, 0, s, a);
-  } else {
-    if (vec) hipLaunchKernelGGL((block_norm_kernel<XF, Y, NT, V, true>), dim3(grid), block, 0, s, a);
-    else hipLaunchKernelGGL((block_norm_kernel<XF, Y, NT, V, false>), dim3(grid), block, 0, s, a);
-  }
+  if (vec) hipLaunchKernelGGL((block_norm_kernel<XF, Y, NT, V, true>), dim3(grid), block, 0, s, a);
+  else hipLaunchKernelGGL((block_norm_kernel<XF, Y, NT, V, false>), dim3(grid), block, 0, s, a);
+}
+
+template <bool XF, int Y, int NT, int V>
+void launch_back(const NormArgs& a, bool vec, unsigned grid, hipStream_t s) {
+  const dim3 block(back_threads(NT, V));
+  if (vec) hipLaunchKernelGGL((block_norm_back_kernel<XF, Y, NT, V, true>), dim3(grid), block, 0, s, a);
+  else hipLaunchKernelGGL((block_norm_back_kernel<XF, Y, NT, V, false>), dim3(grid), block, 0, s, a);
 }
 
 template <bool BACK, bool XF, int Y>
 void launch_typed(const NormArgs& a, Shape sh, bool vec, unsigned grid, hipStream_t s) {
-  switch (sh.nt * sh.v) {
-    case 64: return launch_shape<BACK, XF, Y, 64, 1>(a, vec, grid, s);
-    case 256: return launch_shape<BACK, XF, Y, 256, 1>(a, vec, grid, s);
-    case 512: return launch_shape<BACK, XF, Y, 512, 1>(a, vec, grid, s);
-    case 1024: return launch_shape<BACK, XF, Y, 1024, 1>(a, vec, grid, s);
-    default: return launch_shape<BACK, XF, Y, 1024, 2>(a, vec, grid, s);
+  const int shape = sh.nt * 8 + sh.v;
+  if constexpr (BACK) {
+    switch (shape) {
+      case 64 * 8 + 1: return launch_back<XF, Y, 64, 1>(a, vec, grid, s);
+      case 256 * 8 + 1: return launch_back<XF, Y, 256, 1>(a, vec, grid, s);
+      case 256 * 8 + 2: return launch_back<XF, Y, 256, 2>(a, vec, grid, s);
+      case 512 * 8 + 2: return launch_back<XF, Y, 512, 2>(a, vec, grid, s);
+      default: return launch_back<XF, Y, 512, 4>(a, vec, grid, s);
+    }
+  } else {
+    switch (shape) {
+      case 64 * 8 + 1: return launch_forward<XF, Y, 64, 1>(a, vec, grid, s);
+      case 256 * 8 + 1: return launch_forward<XF, Y, 256, 1>(a, vec, grid, s);
+      case 256 * 8 + 2: return launch_forward<XF, Y, 256, 2>(a, vec, grid, s);
+      case 1024 * 8 + 1: return launch_forward<XF, Y, 1024, 1>(a, vec, grid, s);
+      default: return launch_forward<XF, Y, 1024, 2>(a, vec, grid, s);
+    }
   }
 }
 
@@ -477,9 +521,9 @@ int rows_per_group(Shape sh) { return sh.nt < 256 ? 256 / sh.nt : 1; }
 // Workgroups of the backward pass: enough to fill the CUs, few enough that
 // their partial column sums stay small next to the rows.
 int back_groups(int T, int H) {
-  const Shape sh = shape_of(H);
-  const int rows = rows_per_group(sh);
-  const int most = device_num_cus() * (sh.nt >= 512 ? 2 : 4);
+  const Shape sh = back_shape_of(H);
+  const int rows = back_threads(sh.nt, sh.v) / sh.nt;
+  const int most = device_num_cus() * (sh.nt == 256 ? 2 : 1);
   return T > 0 ? std::min(most, (T - 1) / rows + 1) : 0;
 }
 
@@ -498,13 +542,13 @@ hipError_t launch_block_norm(const moe_block& B, void* out, void* n, hipStream_t
 }
 
 size_t block_norm_backward_workspace(int T, int H) {
-  return (size_t)3 * back_groups(T, H) * rows_per_group(shape_of(H)) * H * sizeof(float);
+  return (size_t)3 * back_groups(T, H) * H * sizeof(float);
 }
 
 hipError_t launch_block_norm_backward(const moe_block& B, const void* go, const void* gn, void* dx,
                                       void* dy, void* dgate, float* dwp, float* dwn, float* part,
                                       hipStream_t s) {
-  const Shape sh = shape_of(B.H);
+  const Shape sh = back_shape_of(B.H);
   NormArgs a = args_of(B);
   a.go = go;
   a.gn = gn;
@@ -513,7 +557,7 @@ hipError_t launch_block_norm_backward(const moe_block& B, const void* go, const 
   a.dgate = dgate;
   a.part = part;
   const int groups = back_groups(B.T, B.H);
-  a.parts = groups * rows_per_group(sh);
+  a.parts = groups;
   const bool token = B.gate_kind == MOE_GATE_TOKEN;
   if (groups > 0) {
     const bool vec = vectors_ok(B, {B.x, B.y, B.w_post, B.w_next, token ? nullptr : B.gate, go, gn,

@@ -42,20 +42,24 @@ __device__ __forceinline__ void store1(void* p, size_t i, float v) {
   else reinterpret_cast<__bf16*>(p)[i] = (__bf16)v;
 }
 
-// Stores eight values from element index i on (16-byte aligned).
-template <bool F32>
+// Stores eight values from element index i on (16-byte aligned).  PAST: with a
+// streaming policy, so that rows written do not drive out what is read again.
+template <bool F32, bool PAST = false>
 __device__ __forceinline__ void store8(void* p, size_t i, const float (&v)[8]) {
+  auto put = [&](u32x4* q, u32x4 w) {
+    if constexpr (PAST) __builtin_nontemporal_store(w, q);
+    else *q = w;
+  };
   if constexpr (F32) {
-    float* q = reinterpret_cast<float*>(p) + i;
+    u32x4* q = reinterpret_cast<u32x4*>(reinterpret_cast<float*>(p) + i);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      reinterpret_cast<u32x4*>(q)[h] =
-          u32x4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
-                __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])};
+      put(q + h, u32x4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
+                       __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])});
   } else {
-    *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p) + i) =
+    put(reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p) + i),
         u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-              pack_bf16(v[6], v[7])};
+              pack_bf16(v[6], v[7])});
   }
 }
 
