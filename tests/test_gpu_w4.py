@@ -87,7 +87,8 @@ def check(lib, c, swiglu=False, y_dtype="f32"):
 DENSE = [(1, 1, 32, 32), (1, 16, 128, 128), (1, 17, 96, 32), (3, 33, 192, 64), (1, 4096, 2048, 128),
          (2, 100, 4096, 64), (5, 1001, 224, 32), (16, 48, 640, 128), (17, 257, 1024, 256),
          (32, 64, 2048, 32), (33, 31, 512, 64), (64, 515, 768, 128), (65, 80, 384, 128),
-         (200, 130, 1024, 1024), (4, 20000, 256, 64), (40, 17000, 160, 32), (20, 16500, 128, 128)]
+         (200, 130, 1024, 1024), (3, 40, 9216, 128), (20, 50, 5120, 64), (1, 33, 20480, 1024), (12, 20, 4224, 32),
+         (4, 20000, 256, 64), (40, 17000, 160, 32), (20, 16500, 128, 128)]
 
 
 @pytest.mark.parametrize("T,N,K,G", DENSE)
@@ -103,7 +104,8 @@ def test_dense_swiglu(lib, T, N, K, G):
 
 
 EXPERTS = [(1, 64, 128, 32, 8, 2), (5, 50, 256, 64, 3, 3), (32, 96, 512, 128, 16, 4), (40, 33, 224, 32, 4, 2),
-           (64, 48, 256, 128, 2, 1), (200, 32, 128, 128, 5, 2), (1, 40, 128, 64, 1, 1), (256, 18, 96, 32, 64, 8)]
+           (64, 48, 256, 128, 2, 1), (200, 32, 128, 128, 5, 2), (1, 40, 128, 64, 1, 1), (256, 18, 96, 32, 64, 8),
+           (2, 24, 18432, 128, 3, 2), (60, 20, 5120, 64, 4, 4)]
 
 
 @pytest.mark.parametrize("T,N,K,G,E,k", EXPERTS)
