@@ -3,12 +3,23 @@
 // for a few rows x at once, with one matrix or the routed experts' matrices.
 //
 // Every weight is used for at most a few x rows, so its bytes (K/2 a row, plus
-// scales) bound the product.  v_mfma_f32_16x16x32_bf16 takes the x rows as its
-// 16 A rows and 16 weight rows as its B columns: the products q x are exact (a
-// 4-bit integer and a BF16 value), the matrix core adds them in FP32, and a
-// lane ends with four x rows of one weight row, so a group is finished with
-// one scale per lane:  y += s (sum q x - z sum x),  the sum of x by an MFMA
+// scales) are what it cannot do without.  v_mfma_f32_16x16x32_bf16 takes x rows
+// as its 16 A rows and 16 weight rows as its B columns: the products q x are
+// exact (a 4-bit integer and a BF16 value), the matrix core adds them in FP32,
+// and a lane ends with four x rows of one weight row, so a group is finished
+// with one scale per lane:  y += s (sum q x - z sum x),  the sum of x by an MFMA
 // against ones.
+//
+// A wavefront takes a part of K of a tile of 16 weight rows and requests all of
+// it together, with the part's scales, which lie side by side in their rows
+// and go through its own LDS (read one here and one there by the lanes that
+// use them they cost a cache line each: 84.6 us against 46.6 without them, for
+// the first product below).  Many short wavefronts keep the loads of a CU in
+// flight and even out by themselves; persistent workgroups with x in LDS and a
+// ring of steps in flight took 59 us.  What bounds it is the issue of vector
+// instructions, about 160 for 256 inputs of 16 rows (56 convert the codes, 48
+// finish four groups), 38% of the issue slots over the whole kernel, and the
+// waits around them.
 //
 // A code becomes BF16 without a table: as an E4M3 byte the codes 0..15 stand
 // for 0..15 times 2^-9 (eight subnormals and the first binade), which the
@@ -116,14 +127,6 @@ __device__ __forceinline__ int entries_of(Lists& s, const W4Args& a, int e) {
   return count;
 }
 
-// ---------------------------------------------------------------------------
-// Up to 16 x rows.  A wavefront takes kPart inputs of a tile of 16 weight rows,
-// once, and requests all of them together (512 bytes of each row), with the
-// part's scales, which go through its own LDS; x follows from the caches step
-// by step.  There is no loop to keep fed: many short wavefronts keep every
-// CU's loads in flight and even out by themselves.
-// ---------------------------------------------------------------------------
-
 // Waits for the wavefront's own LDS accesses and for the other wavefronts;
 // global loads stay in flight.
 __device__ __forceinline__ void lds_barrier() {
@@ -161,15 +164,18 @@ __device__ __forceinline__ u32x4 rotate16(u32x4 v) {
                  dpp_u32<0x120 + 16 - N>(v[2]), dpp_u32<0x120 + 16 - N>(v[3])};
 }
 
-// Inputs of a wavefront's part, and wavefronts of a workgroup at most (with
-// four sets of x rows the registers are worth more than the wavefronts).
-// Dense products take parts of 256: 60 us for 40961 x 7168 and 5 x rows, 74
-// and 70 with parts of 512 and 1024.  With routed experts every workgroup
-// first lists its expert's entries, which longer parts spread over more work:
-// 57 us for the gate and up products of 32 tokens and 128 experts (1536 x 2048
-// each, top-8), 69 and 103 with parts of 512 and 256.
+// Inputs of a wavefront's part, and wavefronts of a workgroup at most; they
+// take the parts of K in turn, the same ones whatever the number of x rows, so
+// that a row's sums do not depend on the batch.
+// Dense products take parts of 256: 51.0 us for 40961 x 7168 (G = 64, float
+// scales, zero points) and 5 x rows; with parts of 512 52.3, with 4 and 16
+// wavefronts 52.8 and 63.4, with the next part's weights requested ahead 51.8.
+// With routed experts every workgroup first lists its expert's entries, which
+// longer parts spread over more work: 55.6 us for the gate and up products of
+// 32 tokens and 128 experts (1536 x 2048 each, top-8), 67 and 103 with parts of
+// 512 and 256.
 __host__ __device__ constexpr int part_inputs(int sets, bool routed) { return sets == 1 && routed ? 1024 : 256; }
-__host__ __device__ constexpr int most_waves(int sets) { return sets == 4 ? 8 : 16; }
+constexpr int kTileWaves = 8;
 
 // Dwords of a row of `groups` scales (or zero points) in LDS: an odd number,
 // so that 16 rows start in different banks.
@@ -219,7 +225,7 @@ __device__ __forceinline__ int log2_of(int v) { return 31 - __clz(v); }
 // and the sums of x take one MFMA for both.  The order of a row's sums is the
 // same whatever the number of sets.
 template <int SETS, bool ROUTED, int GM, bool SF, bool ZP, bool DW>
-__global__ __launch_bounds__(most_waves(SETS) * kWave) void w4_tile_kernel(W4Args a) {
+__global__ __launch_bounds__(kTileWaves * kWave) void w4_tile_kernel(W4Args a) {
   extern __shared__ __align__(16) uint32_t lds[];
   __shared__ Lists s_entries;
   constexpr int kSize = SF ? 4 : 2, kPer = DW ? 4 / kSize : 1, kPerZ = DW ? 4 : 1;
@@ -462,7 +468,7 @@ hipError_t launch_w4_linear(const moe_w4_weights& W, const uint16_t* x, const in
   const int rows = ids ? (3 * a.entries + a.E - 1) / a.E : T;
   const int sets = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   const int inputs = part_inputs(sets, ids != nullptr);
-  const int waves = std::min(most_waves(sets), (a.K + inputs - 1) / inputs);
+  const int waves = std::min(kTileWaves, (a.K + inputs - 1) / inputs);
   const int part = std::min(inputs / 32, std::max(1, inputs >> (5 + a.group_shift)));
   // whole dwords of scales in a row and in a part of it
   const bool dwords = (sf || (a.groups % 2 == 0 && part % 2 == 0)) &&
