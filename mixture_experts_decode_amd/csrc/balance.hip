@@ -109,11 +109,11 @@ __device__ __forceinline__ void load_scores(float (&v)[PER], const BalanceArgs& 
   }
 }
 
-// v -> exp(v - max), 0 past E; returns the sum, the maximum by reference (-inf
-// if the row has no score).  The difference is taken first: it is exact near
-// the maximum and finite wherever the result is not 0, also for rows of the
-// type's lowest value; 2^x is the hardware's, off by one unit in the last
-// place.
+// v -> exp(v - max), 0 past E; returns the sum (0 if the row has no score, else
+// at least 1 or NaN), the maximum by reference.  The difference is taken first:
+// it is exact near the maximum and finite wherever the result is not 0, also
+// for rows of the type's lowest value; 2^x is the hardware's, off by one unit
+// in the last place.
 template <int LPR, int PER, bool VEC>
 __device__ __forceinline__ float exponentials(float (&v)[PER], float& m, int E, int li) {
   if (E < LPR * PER) {
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(kBalanceBlock) void balance_kernel(BalanceArgs a) {
         id[q] = a.ids[(size_t)t * a.k + min(li + LPR * q, a.k - 1)];
       }
       const float sum = exponentials<LPR, PER, VEC>(v, m, a.E, li);
-      if (m == -INFINITY) continue;
+      if (sum == 0.0f) continue;
       const float inv = __builtin_amdgcn_rcpf(sum);
 #pragma unroll
       for (int i = 0; i < PER; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
@@ -379,7 +379,7 @@ __global__ __launch_bounds__(kBackBlock) void router_back_kernel(BalanceArgs a) 
     if (live) {
       float m;
       const float sum = exponentials<LPR, PER, VEC>(d, m, a.E, li);
-      const float inv = m == -INFINITY ? 0.0f : __builtin_amdgcn_rcpf(sum);
+      const float inv = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
       float fp = 0.0f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(kBackBlock) void router_back_kernel(BalanceArgs a) 
         fp = fmaf(f[i], d[i], fp);
       }
       fp = group_sum<LPR>(fp);
-      const float lse = m == -INFINITY ? 0.0f : m + log_of(sum);
+      const float lse = sum == 0.0f ? 0.0f : m + log_of(sum);
       const float base = fmaf(gz, lse, -(gl * fp));
 #pragma unroll
       for (int i = 0; i < PER; ++i) d[i] *= fmaf(gl, f[i], base);
@@ -479,7 +479,7 @@ bool single_block(int T, int E, int S) { return S <= 4 && T <= 4 * (kBalanceBloc
 
 int blocks_of(int T, int E) {
   const int rows = block_rows_of(T, E);
-  return (int)(((long long)T + rows - 1) / rows);
+  return std::max(1, (int)(((long long)T + rows - 1) / rows));   // one clears the counters if there is no token
 }
 
 int chunks_of(int E) { return (E + kWave - 1) / kWave; }

@@ -340,3 +340,37 @@ def test_refusals(lib):
         lib.router_backward(c["scores"], c["ids"])
     with pytest.raises(lib.MoeError):   # weights without their gradient
         lib.router_backward(c["scores"], c["ids"], weights=c["weights"])
+
+
+def test_no_tokens_many_sequences(lib):
+    """An empty batch that is split over more sequences than one workgroup takes."""
+    scores = torch.empty((0, 130), device="cuda")
+    ids = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    loss, counts, tokens = lib.balance_loss(scores, ids,
+                                            seq_offsets=torch.zeros(8, dtype=torch.int32, device="cuda"))
+    assert loss.shape == (7, 2) and not loss.any() and not counts.any() and not tokens.any()
+
+
+@pytest.mark.parametrize("T,S", [(40, 2), (3000, 6)])
+@pytest.mark.parametrize("other", [0.25, -math.inf])
+def test_nan_scores_reach_their_sequence_alone(lib, T, S, other):
+    c = make(T, 16, 2, S=S, tail=False, seed=5)
+    cuts = c["offsets"].tolist()
+    q = max(range(S), key=lambda i: cuts[i + 1] - cuts[i])
+    row = (cuts[q] + cuts[q + 1]) // 2
+    c["scores"][row] = other
+    clean = lib.balance_loss(c["scores"], c["ids"], seq_offsets=c["offsets"])[0]
+    c["scores"][row, 3] = float("nan")
+    loss = lib.balance_loss(c["scores"], c["ids"], seq_offsets=c["offsets"])[0]
+    for i in range(S):
+        if i == q:
+            assert bool(loss[i].isnan().all())
+        else:
+            assert torch.equal(loss[i], clean[i])
+
+
+def test_first_tensor_by_keyword(lib):
+    c = make(33, 16, 2)
+    a = lib.balance_loss(c["scores"], c["ids"])
+    b = lib.balance_loss(ids=c["ids"], scores=c["scores"], stream=torch.cuda.current_stream())
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
