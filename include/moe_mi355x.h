@@ -366,7 +366,8 @@ moe_status moe_check_routing(const int32_t* topk_ids, int32_t T, int32_t k, int3
  *   loss[s][1]   = (1/n_s) sum_t lse(scores[t])^2        (the z loss)
  * A sequence without a counting token has counts 0 and losses 0.
  *   scores      device [T][E] float32; -inf takes an expert out of the softmax,
- *               a token with no other score does not count
+ *               a token with no other score does not count.  A NaN makes its
+ *               sequence's losses NaN
  *   topk_ids    device [T][k] int32 (moe_topk_route's)
  *   token_mask  device [T] bytes or NULL: a token with a 0 does not count, its
  *               scores and ids are not read
@@ -448,7 +449,8 @@ typedef struct {
  * norm before the next block.  Without y it is that last norm alone: n of x.
  *   out  device [T][H] x_dtype, contiguous; NULL exactly when y is NULL.  It may
  *        be x itself when x_stride == H
- *   n    device [T][H] x_dtype, contiguous; NULL exactly when w_next is NULL
+ *   n    device [T][H] x_dtype, contiguous; NULL exactly when w_next is NULL.
+ *        It may be x itself likewise where out is not; out and n are two buffers
  * Statistics and sums are FP32; out and n are rounded once each, n from the
  * unrounded out.  The mean square of a row must be finite in FP32; with eps 0
  * a zero row gives NaN.  T == 0 is a no-op.
@@ -513,10 +515,13 @@ typedef struct {
  *   x  device BF16 [T][K] or [T][k][K], 16-byte aligned
  *   y  device [T][N'] or [T][k][N'], N' = N or N/2, y_dtype, rounded once
  * The products code * x are exact, the sums FP32, in an order that depends on
- * the sizes only, not on which tokens share an expert.
+ * the sizes only, not on which tokens share an expert; of a dense product it
+ * does not depend on T either.  A group's sums of code * x and zero * x are
+ * taken apart, so both must be finite in FP32: a row of x with an infinity or a
+ * NaN gives infinities and NaN in its own outputs.  y must not overlap x.
  * T == 0 is a no-op.  An id outside [0, E) is read as matrix 0.  Limits
- * (MOE_ERR_UNSUPPORTED): N <= 2^24, K <= 2^20, E <= 1024, T <= 2^21 and, with
- * ids, T*k <= moe_decode_max_entries().
+ * (MOE_ERR_UNSUPPORTED): N <= 2^24, K <= 2^20, N (K/G) < 2^31, E <= 1024,
+ * T <= 2^20 and, with ids, T*k <= moe_decode_max_entries().
  */
 moe_status moe_w4_linear(const moe_w4_weights* W, const uint16_t* x, const int32_t* topk_ids,
                          const float* topk_weights, int32_t T, int32_t k, int32_t x_per_slot,

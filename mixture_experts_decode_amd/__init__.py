@@ -356,18 +356,21 @@ def check_routing(ids, num_experts, result=None, stream=None):
 def _on_device(fn):
     """Run a binding call on its first tensor's device and, with `stream`,
     with that stream made torch's current one (as _on_stream)."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def wrapped(first, *args, stream=None, **kwargs):
+    def wrapped(*args, stream=None, **kwargs):
+        first = args[0] if args else kwargs[name]
         dev = first.get_device()
         if dev < 0:
             raise ValueError(f"{fn.__name__}: tensors must be on a GPU, not on {first.device}")
         if stream is None and dev == torch.cuda.current_device():
-            return fn(first, *args, **kwargs)
+            return fn(*args, **kwargs)
         if stream is not None and stream.device != first.device:
             raise ValueError(f"{fn.__name__}: the stream belongs to {stream.device}, the tensors to "
                              f"{first.device}")
         with torch.cuda.device(dev), torch.cuda.stream(stream):
-            return fn(first, *args, **kwargs)
+            return fn(*args, **kwargs)
     return wrapped
 
 
@@ -623,6 +626,7 @@ def _w4_linear(x, W, ids, weights, swiglu, y, y_dtype):
         k = ids.shape[1]
         shape = (t, k, outs)
     if y is None:
+        _need(y_dtype in DT, f"y_dtype: one of {list(DT)}")
         y = x.new_empty(shape, dtype=torch.float32 if y_dtype == "f32" else torch.bfloat16)
     else:
         _tensor(y, "y", x, shape, tuple(_ROWS))

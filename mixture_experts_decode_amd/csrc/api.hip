@@ -195,7 +195,7 @@ constexpr int32_t kMaxBalanceTokens = 1 << 30;
 constexpr int32_t kMaxSequences = 1 << 20;
 constexpr int32_t kMaxW4Rows = 1 << 24;
 constexpr int32_t kMaxW4Cols = 1 << 20;
-constexpr int32_t kMaxW4Tokens = 1 << 21;
+constexpr int32_t kMaxW4Tokens = 1 << 20;   // 32 to a grid row
 
 moe_status check_balance_sizes(int32_t T, int32_t E, int32_t k, int32_t S) {
   if (T < 0 || E < 1 || E > kMaxExpertsTotal || k < 1 || k > E || k > 64 || S < 1)
@@ -492,8 +492,8 @@ moe_status moe_block_norm(const moe_block* B, void* out, void* n, void* stream) 
   if (B->T == 0) return MOE_OK;
   if (!B->x || (B->y == nullptr) != (out == nullptr) || (B->w_next == nullptr) != (n == nullptr))
     return MOE_ERR_INVALID_ARG;
-  if (!out && !n) return MOE_ERR_INVALID_ARG;
   if (out == B->x && B->x_stride != B->H) return MOE_ERR_INVALID_ARG;
+  if (out == n) return MOE_ERR_INVALID_ARG;
   return from_hip(moe::launch_block_norm(*B, out, n, as_stream(stream)));
 }
 
@@ -547,7 +547,11 @@ moe_status moe_w4_linear(const moe_w4_weights* W, const uint16_t* x, const int32
   if (!topk_ids && (W->num_mats != 1 || k != 1 || x_per_slot || topk_weights))
     return MOE_ERR_INVALID_ARG;
   if (!W->q || !W->scale || !x || !y || !aligned16(W->q) || !aligned16(x)) return MOE_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(W->scale) % (W->scale_dtype == MOE_DT_F32 ? 4 : 2) ||
+      reinterpret_cast<uintptr_t>(y) % (y_dtype == MOE_DT_F32 ? 4 : 2))
+    return MOE_ERR_INVALID_ARG;
   if (W->rows > kMaxW4Rows || W->cols > kMaxW4Cols || W->num_mats > kMaxExpertsTotal ||
+      (int64_t)W->rows * (W->cols / W->group) > INT32_MAX ||   // scales of a matrix, counted in 32 bits
       T > kMaxW4Tokens || (topk_ids && (int64_t)T * k > kDecodeMaxEntries))
     return MOE_ERR_UNSUPPORTED;
   return from_hip(moe::launch_w4_linear(*W, x, topk_ids, topk_weights, T, k, x_per_slot, swiglu, y,

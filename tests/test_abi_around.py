@@ -88,6 +88,7 @@ def test_block_norm_refusals(moe):
     assert f(block(moe, y=None), None, DUMMY, None) == bad    # w_post without y
     assert f(block(moe, y=None, w_post=None, w_next=None), None, None, None) == bad
     assert f(block(moe, x_stride=72), DUMMY, P(1 << 16), None) == bad   # in place with another stride
+    assert f(block(moe), P(1 << 16), P(1 << 16), None) == bad                 # out and n are two buffers
     assert f(block(moe, H=16385, x_stride=16385, y_stride=16385), P(1 << 16), DUMMY,
              None) == moe.ERR_UNSUPPORTED
     assert f(block(moe, x_dtype=0, y_dtype=1), P(1 << 16), DUMMY, None) == moe.ERR_UNSUPPORTED
@@ -140,10 +141,12 @@ def test_w4_linear_refusals(moe):
     for kw in (dict(rows=0), dict(cols=0), dict(num_mats=0), dict(group=0), dict(T=-1), dict(k=0),
                dict(scale_dtype=3), dict(ydt=2), dict(slots=2), dict(swiglu=-1), dict(rows=31, swiglu=1),
                dict(num_mats=2), dict(k=2), dict(slots=1), dict(wts=DUMMY), dict(q=None), dict(q=4104),
-               dict(scale=None), dict(x=None), dict(x=P(4100)), dict(y=None)):
+               dict(scale=None), dict(x=None), dict(x=P(4100)), dict(y=None), dict(scale=4097),
+               dict(scale=4098, scale_dtype=0), dict(y=P(4098)), dict(y=P(4097), ydt=1)):
         assert w4(moe, **kw) == moe.ERR_INVALID_ARG, kw
     for kw in (dict(group=16), dict(group=48, cols=96), dict(cols=96), dict(rows=(1 << 24) + 1),
                dict(cols=1 << 21), dict(num_mats=1025, ids=DUMMY), dict(T=(1 << 21) + 1),
+               dict(T=(1 << 20) + 1), dict(rows=1 << 17, cols=1 << 20, group=64),
                dict(T=1025, k=2, ids=DUMMY, num_mats=4)):
         assert w4(moe, **kw) == moe.ERR_UNSUPPORTED, kw
     assert w4(moe, T=0, x=None, y=None) == moe.OK
