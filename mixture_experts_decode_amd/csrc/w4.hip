@@ -317,6 +317,8 @@ __global__ __launch_bounds__(kTileWaves * kWave) void w4_tile_kernel(W4Args a) {
       for (int h = 0; h < kHalves; ++h) {
         __builtin_amdgcn_sched_barrier(0);   // a half's temporaries at a time
         const int kh = k0 + 128 * h;
+        // a long part's halves behind K (experts of 2048 x 768, 32 tokens: 47.3 -> 44.8 us)
+        if (ROUTED && !WHOLE && kh >= a.K) break;
         if (h + kAhead < kHalves) load_x(x[(h + kAhead) % (kAhead + 1)], h + kAhead);
         // a group of 128 or more spans the half: each lane keeps its own 32
         // inputs of it, x is read to match
