@@ -350,3 +350,11 @@ def test_refusals(lib):
         lib.block_norm(c["x"])
     with pytest.raises(lib.MoeError):  # FP32 stream with a BF16 block
         lib.block_norm(c["x"].float(), c["y"], w_next=c["w_next"].float())
+
+
+@pytest.mark.parametrize("H", [4104, 5120, 8192, 8191])
+@pytest.mark.parametrize("kind", range(len(KINDS)))
+def test_forward_more_rows_than_cus(lib, H, kind):
+    """Rows of this length take another launch shape in a batch of this size."""
+    x, y, gate, post, nxt = KINDS[kind]
+    check_forward(lib, make(300, H, x, y, gate, post, nxt, seed=H + kind))
