@@ -12,9 +12,9 @@
 // or 64 lanes takes a row with up to 16 values per lane: four rows per
 // wavefront at the usual E, reductions of four DPP steps, each score read
 // once.  65536 tokens x 256 experts, top-8, 24 sequences: 20 us for the rows
-// (69 MB, 3.5 TB/s: one workgroup per CU, see block_rows_of) and 5 us for the
+// (69 MB, 3.5 TB/s: one workgroup per CU, see block_rows_of) and 6 us for the
 // partial sums; the gradient 36 us (141 MB, 3.9 TB/s).  32 tokens x 128 experts
-// 4.3 us, the gradient of 333 tokens 4.6 us: a chain of loads and reductions.
+// 4.1 us, the gradient of 333 tokens 4.6 us: a chain of loads and reductions.
 
 #include <algorithm>
 
@@ -141,7 +141,9 @@ __device__ __forceinline__ float exponentials(float (&v)[PER], float& m, int E, 
 // log of a row's sum, which is at least 1.
 __device__ __forceinline__ float log_of(float s) { return __builtin_amdgcn_logf(s) * 0.693147180559945309f; }
 
-constexpr int kBalanceBlock = 1024;
+// 512 threads: 4.1 us for 32 tokens x 128 experts and 8.1 us for 2048, with 1024
+// 4.5 and 9.2; 25.3 and 25.0 us for 65536 x 256.
+constexpr int kBalanceBlock = 512;
 
 // Loss of one sequence from its column sums (p and c of expert e in LDS) and
 // its z sum and token count; every thread of the workgroup calls it.
@@ -468,7 +470,7 @@ int lanes_of(int E) { return E <= 256 ? 16 : E <= 512 ? 32 : 64; }
 
 // Tokens per workgroup of the forward pass: whole rounds of its groups, and
 // one workgroup per CU, whose partial sums then stay few (65536 x 256, 24
-// sequences: 25.0 us, with two and four per CU 29.5 and 38.0).
+// sequences, 1024 threads: 25.0 us, with two and four per CU 29.5 and 38.0).
 int block_rows_of(int T, int E) {
   const int round = kBalanceBlock / lanes_of(E);
   const int cus = device_num_cus();
@@ -476,9 +478,10 @@ int block_rows_of(int T, int E) {
   return rounds * round;
 }
 
-// All tokens in one workgroup and one launch: up to four rounds of its
-// groups, and few sequences, which it takes one after the other.
-bool single_block(int T, int E, int S) { return S <= 4 && T <= 4 * (kBalanceBlock / lanes_of(E)); }
+// All tokens in one workgroup and one launch: up to eight rounds of its
+// groups (256 tokens x 128 experts: 7.2 us, in two launches 7.8; 512 tokens
+// 10.8 and 8.2), and few sequences, which it takes one after the other.
+bool single_block(int T, int E, int S) { return S <= 4 && T <= 8 * (kBalanceBlock / lanes_of(E)); }
 
 int blocks_of(int T, int E) {
   const int rows = block_rows_of(T, E);
