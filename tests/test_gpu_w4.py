@@ -266,3 +266,16 @@ def test_refusals(lib):
     big = make(4, 32, 96, 96)
     with pytest.raises(lib.MoeError):   # groups of a power of two
         lib.w4_linear(lib.W4Weights(big["q"], big["scale"]), big["x"])
+
+
+@pytest.mark.parametrize("T,bad", [(5, 2), (16, 15), (37, 20)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_bad_row_of_x_stays_its_own(lib, T, bad, value):
+    c = make(T, 40, 448, 64, zero=True)
+    W = lib.W4Weights(c["q"], c["scale"], c["zero"])
+    clean = lib.w4_linear(W, c["x"])
+    c["x"][bad, 100] = value
+    got = lib.w4_linear(W, c["x"])
+    keep = torch.arange(T, device="cuda") != bad
+    assert torch.equal(got[keep], clean[keep])
+    assert not bool(got[bad].isfinite().any())
