@@ -31,12 +31,6 @@ template <> struct Raw8<true> {
 
 // One element of a row at element index i.
 template <bool F32>
-__device__ __forceinline__ float load1(const void* p, size_t i) {
-  if constexpr (F32) return reinterpret_cast<const float*>(p)[i];
-  else return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << 16);
-}
-
-template <bool F32>
 __device__ __forceinline__ void store1(void* p, size_t i, float v) {
   if constexpr (F32) reinterpret_cast<float*>(p)[i] = v;
   else reinterpret_cast<__bf16*>(p)[i] = (__bf16)v;

@@ -155,15 +155,6 @@ __device__ __forceinline__ u32x4 even_odd(u32x4 v) {
                __builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
 }
 
-// Lane i of each row of 16 gets lane i + N's value.
-template <int N>
-__device__ __forceinline__ u32x4 rotate16(u32x4 v) {
-  if constexpr (N == 0) return v;
-  else
-    return u32x4{dpp_u32<0x120 + 16 - N>(v[0]), dpp_u32<0x120 + 16 - N>(v[1]),
-                 dpp_u32<0x120 + 16 - N>(v[2]), dpp_u32<0x120 + 16 - N>(v[3])};
-}
-
 // Inputs of a wavefront's part, and wavefronts of a workgroup at most; they
 // take the parts of K in turn.  Dense products have the same parts whatever the
 // number of x rows, so that a row's sums do not depend on the batch.
