@@ -234,10 +234,13 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_kernel(NormArg
 __host__ __device__ constexpr int back_threads(int nt, int v) { return nt == kWave ? 1024 / v : nt; }
 
 // The backward pass, with x the stored o:
-//   D  = do + r w_next (.) dn - o r^3/H <w_next (.) dn, o>      r = 1/rms(o)
+//   D  = do + r (w_next (.) dn - o c),  c = r^2/H <w_next (.) dn, o>   r = 1/rms(o)
 //   dx = res_scale D,   q = g (.) D,   dg = D (.) b
-//   dy = r w_post (.) q - y r^3/H <w_post (.) q, y>             r = 1/rms(y)
+//   dy = r (w_post (.) q - y c),        c = r^2/H <w_post (.) q, y>    r = 1/rms(y)
 //   dw_next = sum_t dn o r,  dw_post = sum_t q y r
+// c is about 1 / rms, as r is, and formed from the product with the row, which
+// is about rms, one r after the other: r^3 alone would leave FP32's range for
+// rows of 1e13 and of 1e-13.
 // The three sums of squares and products that D needs come from one
 // reduction over the row, the product that dy (and a token's gate) needs from
 // a second one.  A workgroup walks rows with a fixed stride and keeps its
@@ -297,12 +300,12 @@ __global__ __launch_bounds__(back_threads(NT, V)) void block_norm_back_kernel(No
         }
       row_sums<NT, 3>(s, lds, half);
       const float r = rsqrtf(fmaf(s[0], a.inv_h, a.eps));
-      const float c = r * r * r * (s[1] * a.inv_h);
+      const float c = r * (r * (s[1] * a.inv_h));
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          d[v][i] += fmaf(r * w[v][i], g[v][i], -(o[v][i] * c));
+          d[v][i] = fmaf(r, fmaf(w[v][i], g[v][i], -(o[v][i] * c)), d[v][i]);
           swn[v][i] = fmaf(g[v][i] * o[v][i], r, swn[v][i]);
         }
     } else if (Y != Y_NONE && a.wp) {
@@ -338,7 +341,7 @@ __global__ __launch_bounds__(back_threads(NT, V)) void block_norm_back_kernel(No
         if (a.gate_kind == MOE_GATE_TOKEN && tid == 0)
           reinterpret_cast<float*>(a.dgate)[t] = ry * u[0];
       }
-      const float c = a.wp ? ry * ry * ry * (gt * u[0] * a.inv_h) : 0.0f;
+      const float c = a.wp ? ry * (ry * (gt * u[0] * a.inv_h)) : 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float dg[8];
@@ -348,7 +351,7 @@ __global__ __launch_bounds__(back_threads(NT, V)) void block_norm_back_kernel(No
           dg[i] = d[v][i] * (yn * w[v][i]);
           swp[v][i] = fmaf(q, yn, swp[v][i]);
           sg[v][i] += dg[i];
-          y[v][i] = fmaf(ry * w[v][i], q, -(y[v][i] * c));
+          y[v][i] = ry * fmaf(w[v][i], q, -(y[v][i] * c));
         }
         if (a.gate_kind == MOE_GATE_FULL) store_row<XF, NT, VEC>(dg, a.dgate, row, v, tid, a.H);
         store_row<YF, NT, VEC, true>(y[v], a.dy, row, v, tid, a.H);

@@ -1,0 +1,36 @@
+"""moe_block_norm and its backward pass on rows far from 1, against the
+formulas in float64, at the tolerances of test_gpu_block_norm.py: relative to
+the magnitudes that enter a value, so the rows' scale does not change them."""
+
+import pytest
+
+from test_gpu_block_norm import BF16, C_ROW, EPS, F32, args, close, gradients, make
+
+pytestmark = pytest.mark.gpu
+
+
+def scaled(c, name, scale):
+    c[name] = (c[name].float() * scale).to(c[name].dtype)
+    return c
+
+
+def check_backward(lib, c, eps):
+    got = lib.block_norm_backward(c["grad_out"], c["grad_n"], c["x"], c["y"], res_scale=0.875, eps=eps, **args(c))
+    want, mag = gradients(c, 0.875, eps)
+    for k in want:
+        # column sums add at most one rounding a token and 80 over the workgroups
+        close(got[k], want[k], mag[k], 2 * C_ROW + (c["x"].shape[0] + 80 if got[k].dim() == 1 else 0), k)
+
+
+@pytest.mark.parametrize("T,H", [(3, 200), (2, 1001), (4, 4096), (2, 8192), (2, 9000)])
+@pytest.mark.parametrize("scale,eps", [(1e15, EPS), (3e12, EPS), (1e-14, 0.0), (1e-12, 0.0)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradients_of_loud_and_quiet_rows(lib, T, H, scale, eps, dtype):
+    """The gradient is about 1/rms, whose cube would leave float32.  The stored
+    stream and the block's output are taken one at a time, so that the term in
+    question is not lost beside a larger one."""
+    c = scaled(make(T, H, dtype, None, seed=17), "x", scale)
+    c["grad_out"] = None
+    check_backward(lib, c, eps)
+    for gate in ("channel", "token"):
+        check_backward(lib, scaled(make(T, H, dtype, dtype, gate, nxt=False, seed=18), "y", scale), eps)
