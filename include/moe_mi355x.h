@@ -452,8 +452,9 @@ typedef struct {
  *   n    device [T][H] x_dtype, contiguous; NULL exactly when w_next is NULL.
  *        It may be x itself likewise where out is not; out and n are two buffers
  * Statistics and sums are FP32; out and n are rounded once each, n from the
- * unrounded out.  The mean square of a row must be finite in FP32; with eps 0
- * a zero row gives NaN.  T == 0 is a no-op.
+ * unrounded out.  The mean square of a row must be finite in FP32, and 2^-100
+ * or more where eps is less (with eps 0 a zero row gives NaN).  T == 0 is a
+ * no-op.
  * Sizes: 1 <= H <= 16384 (MOE_ERR_UNSUPPORTED past it), eps >= 0.  Rows are
  * read 16 bytes at a time when H and the strides are multiples of 8 and the
  * pointers 16-byte aligned, by element otherwise.

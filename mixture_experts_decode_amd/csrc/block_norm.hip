@@ -14,6 +14,7 @@
 // 2.7 us, the latency of a load, two reductions and a store.
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 
 #include "internal.h"
@@ -28,6 +29,7 @@ enum YKind { Y_NONE = 0, Y_BF16 = 1, Y_F32 = 2 };
 struct NormArgs {
   int T, H, gate_kind;
   float a, eps, inv_h;
+  float sq_in, sq_out;               // row sums of squares, see squares_of
   long long xs, ys;                  // elements between rows
   const void *x, *y, *wp, *wn, *gate;
   void *out, *n;                     // forward
@@ -154,6 +156,27 @@ __device__ __forceinline__ void row_sums(float (&s)[M], float* lds, int& half) {
   }
 }
 
+// This thread's part of a row's sum of squares, of the values times sq_in = 2^-k
+// with 4^k >= H: it overflows no sooner than the mean square itself, which is
+// the row's sum times sq_out = 4^k / H.  Powers of two change no bits: the sums
+// differ from unscaled ones only where either leaves the normal range.
+template <int V>
+__device__ __forceinline__ float squares_of(const NormArgs& a, const float (&f)[V][8]) {
+  float s = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = f[v][i] * a.sq_in;
+      s = fmaf(q, q, s);
+    }
+  return s;
+}
+
+__device__ __forceinline__ float inv_rms(const NormArgs& a, float squares) {
+  return rsqrtf(fmaf(squares, a.sq_out, a.eps));
+}
+
 template <bool XF, int Y, int NT, int V, bool VEC>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_kernel(NormArgs a) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;   // rows per workgroup
@@ -183,13 +206,9 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_kernel(NormArg
       float y[V][8], w[V][8];
       unpack_all<YF, NT, VEC>(y, yr, tid, a.H);
       if (a.wp) {
-        float s[1] = {0.0f};
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[0] = fmaf(y[v][i], y[v][i], s[0]);
+        float s[1] = {squares_of<V>(a, y)};
         row_sums<NT, 1>(s, lds, half);
-        const float r = rsqrtf(fmaf(s[0], a.inv_h, a.eps));
+        const float r = inv_rms(a, s[0]);
         unpack_all<XF, NT, VEC>(w, pr, tid, a.H);
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -211,13 +230,9 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_kernel(NormArg
       }
     }
     if (a.wn) {
-      float s[1] = {0.0f}, w[V][8];
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] = fmaf(o[v][i], o[v][i], s[0]);
+      float s[1] = {squares_of<V>(a, o)}, w[V][8];
       row_sums<NT, 1>(s, lds, half);
-      const float r = rsqrtf(fmaf(s[0], a.inv_h, a.eps));
+      const float r = inv_rms(a, s[0]);
       unpack_all<XF, NT, VEC>(w, nr, tid, a.H);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -281,10 +296,7 @@ __global__ __launch_bounds__(back_threads(NT, V)) void block_norm_back_kernel(No
     if (a.go) unpack_all<XF, NT, VEC>(d, dr, tid, a.H);
     if constexpr (Y != Y_NONE) {
       unpack_all<YF, NT, VEC>(y, yr, tid, a.H);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[2] = fmaf(y[v][i], y[v][i], s[2]);
+      s[2] = squares_of<V>(a, y);
     }
     if (a.wn) {
       float o[V][8], g[V][8], w[V][8];
@@ -294,12 +306,10 @@ __global__ __launch_bounds__(back_threads(NT, V)) void block_norm_back_kernel(No
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s[0] = fmaf(o[v][i], o[v][i], s[0]);
-          s[1] = fmaf(w[v][i] * g[v][i], o[v][i], s[1]);
-        }
+        for (int i = 0; i < 8; ++i) s[1] = fmaf(w[v][i] * g[v][i], o[v][i], s[1]);
+      s[0] = squares_of<V>(a, o);
       row_sums<NT, 3>(s, lds, half);
-      const float r = rsqrtf(fmaf(s[0], a.inv_h, a.eps));
+      const float r = inv_rms(a, s[0]);
       const float c = r * (r * (s[1] * a.inv_h));
 #pragma unroll
       for (int v = 0; v < V; ++v)
@@ -320,7 +330,7 @@ __global__ __launch_bounds__(back_threads(NT, V)) void block_norm_back_kernel(No
       store_row<XF, NT, VEC, true>(w, a.dx, row, v, tid, a.H);
     }
     if constexpr (Y != Y_NONE) {
-      const float ry = a.wp ? rsqrtf(fmaf(s[2], a.inv_h, a.eps)) : 1.0f;
+      const float ry = a.wp ? inv_rms(a, s[2]) : 1.0f;
       const bool gate_row = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL;
       float w[V][8], g[V][8];
 #pragma unroll
@@ -473,6 +483,10 @@ NormArgs args_of(const moe_block& B) {
   a.a = B.res_scale;
   a.eps = B.eps;
   a.inv_h = 1.0f / (float)B.H;
+  int k = 0;
+  while ((1 << 2 * k) < B.H) ++k;
+  a.sq_in = std::ldexp(1.0f, -k);
+  a.sq_out = std::ldexp(a.inv_h, 2 * k);
   a.xs = B.x_stride;
   a.ys = B.y_stride;
   a.x = B.x;
