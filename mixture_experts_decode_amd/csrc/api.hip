@@ -492,7 +492,7 @@ moe_status moe_block_norm(const moe_block* B, void* out, void* n, void* stream) 
   if (B->T == 0) return MOE_OK;
   if (!B->x || (B->y == nullptr) != (out == nullptr) || (B->w_next == nullptr) != (n == nullptr))
     return MOE_ERR_INVALID_ARG;
-  if (out == B->x && B->x_stride != B->H) return MOE_ERR_INVALID_ARG;
+  if ((out == B->x || n == B->x) && B->x_stride != B->H) return MOE_ERR_INVALID_ARG;
   if (out == n) return MOE_ERR_INVALID_ARG;
   return from_hip(moe::launch_block_norm(*B, out, n, as_stream(stream)));
 }

@@ -150,3 +150,12 @@ def test_w4_linear_refusals(moe):
                dict(T=1025, k=2, ids=DUMMY, num_mats=4)):
         assert w4(moe, **kw) == moe.ERR_UNSUPPORTED, kw
     assert w4(moe, T=0, x=None, y=None) == moe.OK
+
+
+def test_block_norm_in_place_with_a_stride(moe):
+    """Row t of out or n would be written where other rows of x still stand."""
+    f = moe.load().moe_block_norm
+    strided = dict(x_stride=72)
+    assert f(block(moe, **strided), P(1 << 16), DUMMY, None) == moe.ERR_INVALID_ARG
+    assert f(block(moe, y=None, w_post=None, **strided), None, DUMMY, None) == moe.ERR_INVALID_ARG
+    assert f(block(moe, w_next=None, **strided), DUMMY, None, None) == moe.ERR_INVALID_ARG
