@@ -361,7 +361,8 @@ __global__ __launch_bounds__(back_threads(NT, V)) void block_norm_back_kernel(No
           dg[i] = d[v][i] * (yn * w[v][i]);
           swp[v][i] = fmaf(q, yn, swp[v][i]);
           sg[v][i] += dg[i];
-          y[v][i] = ry * fmaf(w[v][i], q, -(y[v][i] * c));
+          // without w_post y itself has no part in dy: an infinity in it would
+          y[v][i] = a.wp ? ry * fmaf(w[v][i], q, -(y[v][i] * c)) : q;
         }
         if (a.gate_kind == MOE_GATE_FULL) store_row<XF, NT, VEC>(dg, a.dgate, row, v, tid, a.H);
         store_row<YF, NT, VEC, true>(y[v], a.dy, row, v, tid, a.H);

@@ -3,6 +3,7 @@ formulas in float64, at the tolerances of test_gpu_block_norm.py: relative to
 the magnitudes that enter a value, so the rows' scale does not change them."""
 
 import pytest
+import torch
 
 from test_gpu_block_norm import BF16, C_ROW, EPS, F32, args, close, gradients, make, reference
 
@@ -62,3 +63,15 @@ def test_rows_up_to_the_largest_mean_square(lib, T, H, scale, eps, dtype):
     # a quiet block joins a quiet stream: out and its norm at that scale
     c = scaled(make(T, H, dtype, F32, post=False, seed=21), "x", scale)
     check_forward(lib, scaled(c, "y", scale), eps)
+
+
+@pytest.mark.parametrize("H", [136, 1001, 2048, 8192])
+@pytest.mark.parametrize("gate", ["none", "channel", "full"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_infinite_block_without_its_norm(lib, H, gate, dtype):
+    """Without w_post and w_next the gradient of y is gate * grad_out whatever y is."""
+    c = make(5, H, dtype, dtype, gate, post=False, nxt=False, seed=22)
+    clean = lib.block_norm_backward(c["grad_out"], None, c["x"], c["y"], res_scale=0.875, eps=EPS, **args(c))
+    c["y"][1, 5], c["y"][3, 7] = float("inf"), float("nan")
+    got = lib.block_norm_backward(c["grad_out"], None, c["x"], c["y"], res_scale=0.875, eps=EPS, **args(c))
+    assert torch.equal(got["y"], clean["y"]) and torch.equal(got["x"], clean["x"])
