@@ -380,9 +380,10 @@ moe_status moe_check_routing(const int32_t* topk_ids, int32_t T, int32_t k, int3
  *               (NULL if that is 0)
  * All sums are FP32 in an order that depends on the sizes only: equal inputs
  * give equal bits.  T == 0 writes zeros.
- * Sizes: 0 <= T <= 2^30, 1 <= E <= 1024, 1 <= k <= min(E, 64), 1 <= S <= 2^20,
- * T*k <= 2^31 - 1.  Errors: MOE_ERR_INVALID_ARG for bad sizes and null or
- * misaligned pointers, MOE_ERR_UNSUPPORTED for sizes past the limits.
+ * Sizes: T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 64), S >= 1, else
+ * MOE_ERR_INVALID_ARG, as for null pointers and ones that are no multiple of
+ * their elements' size; T <= 2^30, S <= 2^20, T*k <= 2^31 - 1, else
+ * MOE_ERR_UNSUPPORTED.
  */
 size_t moe_balance_workspace_bytes(int32_t T, int32_t E, int32_t S);
 
@@ -457,7 +458,8 @@ typedef struct {
  * no-op.
  * Sizes: 1 <= H <= 16384 (MOE_ERR_UNSUPPORTED past it), eps >= 0.  Rows are
  * read 16 bytes at a time when H and the strides are multiples of 8 and the
- * pointers 16-byte aligned, by element otherwise.
+ * pointers 16-byte aligned, by element otherwise (pointers that are no multiple
+ * of their elements' size are refused).
  */
 moe_status moe_block_norm(const moe_block* B, void* out, void* n, void* stream);
 

@@ -7,6 +7,7 @@
 #include <atomic>
 #include <cmath>
 #include <algorithm>
+#include <initializer_list>
 
 #include "moe_mi355x.h"
 #include "moe_mi355x_util.h"
@@ -190,6 +191,15 @@ size_t decode_workspace(const moe_weights* W, int32_t T, int32_t k) {
 
 // ---- operators around the layer -------------------------------------------
 
+// Every pointer (NULL among them) at a multiple of `size` bytes, a power of two.
+bool aligned_to(size_t size, std::initializer_list<const void*> pointers) {
+  for (const void* p : pointers)
+    if (reinterpret_cast<uintptr_t>(p) & (size - 1)) return false;
+  return true;
+}
+
+size_t dtype_size(int32_t dt) { return dt == MOE_DT_F32 ? 4 : 2; }
+
 constexpr int32_t kMaxNormH = 16384;        // a row's registers over one workgroup
 constexpr int32_t kMaxBalanceTokens = 1 << 30;
 constexpr int32_t kMaxSequences = 1 << 20;
@@ -218,6 +228,10 @@ moe_status check_block(const moe_block* B) {
   if (B->x_stride < B->H || (B->y && B->y_stride < B->H)) return MOE_ERR_INVALID_ARG;
   if (B->H > kMaxNormH) return MOE_ERR_UNSUPPORTED;
   if (B->y && B->x_dtype == MOE_DT_F32 && B->y_dtype != MOE_DT_F32) return MOE_ERR_UNSUPPORTED;
+  if (!aligned_to(dtype_size(B->x_dtype), {B->x, B->w_post, B->w_next}) ||
+      !aligned_to(dtype_size(B->y_dtype), {B->y}) ||
+      !aligned_to(B->gate_kind == MOE_GATE_TOKEN ? 4 : dtype_size(B->x_dtype), {B->gate}))
+    return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
@@ -454,6 +468,7 @@ moe_status moe_balance_loss(const float* scores, const int32_t* topk_ids,
   const moe_status st = check_balance_sizes(T, E, k, S);
   if (st != MOE_OK) return st;
   if (!counts || !tokens || !loss || (T > 0 && (!scores || !topk_ids))) return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(4, {scores, topk_ids, seq_offsets, counts, tokens, loss})) return MOE_ERR_INVALID_ARG;
   if (!seq_offsets && S != 1) return MOE_ERR_INVALID_ARG;
   const size_t need = moe::balance_workspace_bytes(T, E, S);
   if (need > 0) {
@@ -479,6 +494,9 @@ moe_status moe_router_backward(const float* scores, const int32_t* topk_ids,
   if (T == 0) return MOE_OK;
   if (!grad_scores || (grad_loss && (!scores || !counts || !tokens)) || (grad_weights && !topk_ids))
     return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(4, {scores, topk_ids, topk_weights, grad_weights, seq_offsets, counts, tokens, grad_loss,
+                      grad_scores}))
+    return MOE_ERR_INVALID_ARG;
   return from_hip(moe::launch_router_backward(scores, topk_ids, topk_weights, grad_weights,
                                               token_mask, seq_offsets, counts, tokens, grad_loss, T,
                                               E, k, S, grad_scores, as_stream(stream)));
@@ -493,7 +511,7 @@ moe_status moe_block_norm(const moe_block* B, void* out, void* n, void* stream) 
   if (!B->x || (B->y == nullptr) != (out == nullptr) || (B->w_next == nullptr) != (n == nullptr))
     return MOE_ERR_INVALID_ARG;
   if ((out == B->x || n == B->x) && B->x_stride != B->H) return MOE_ERR_INVALID_ARG;
-  if (out == n) return MOE_ERR_INVALID_ARG;
+  if (out == n || !aligned_to(dtype_size(B->x_dtype), {out, n})) return MOE_ERR_INVALID_ARG;
   return from_hip(moe::launch_block_norm(*B, out, n, as_stream(stream)));
 }
 
@@ -526,6 +544,11 @@ moe_status moe_block_norm_backward(const moe_block* B, const void* grad_out, con
   } else if (B->gate_kind == MOE_GATE_CHANNEL && !grad_gate) {
     return MOE_ERR_INVALID_ARG;
   }
+  if (!aligned_to(dtype_size(B->x_dtype), {grad_out, grad_n, grad_x}) ||
+      !aligned_to(dtype_size(B->y_dtype), {grad_y}) ||
+      !aligned_to(B->gate_kind == MOE_GATE_FULL ? dtype_size(B->x_dtype) : 4, {grad_gate}) ||
+      !aligned_to(4, {grad_w_post, grad_w_next}))
+    return MOE_ERR_INVALID_ARG;
   return from_hip(moe::launch_block_norm_backward(*B, grad_out, grad_n, grad_x, grad_y, grad_gate,
                                                   grad_w_post, grad_w_next,
                                                   reinterpret_cast<float*>(workspace),
@@ -547,8 +570,8 @@ moe_status moe_w4_linear(const moe_w4_weights* W, const uint16_t* x, const int32
   if (!topk_ids && (W->num_mats != 1 || k != 1 || x_per_slot || topk_weights))
     return MOE_ERR_INVALID_ARG;
   if (!W->q || !W->scale || !x || !y || !aligned16(W->q) || !aligned16(x)) return MOE_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(W->scale) % (W->scale_dtype == MOE_DT_F32 ? 4 : 2) ||
-      reinterpret_cast<uintptr_t>(y) % (y_dtype == MOE_DT_F32 ? 4 : 2))
+  if (!aligned_to(dtype_size(W->scale_dtype), {W->scale}) || !aligned_to(dtype_size(y_dtype), {y}) ||
+      !aligned_to(4, {topk_ids, topk_weights}))
     return MOE_ERR_INVALID_ARG;
   if (W->rows > kMaxW4Rows || W->cols > kMaxW4Cols || W->num_mats > kMaxExpertsTotal ||
       (int64_t)W->rows * (W->cols / W->group) > INT32_MAX ||   // scales of a matrix, counted in 32 bits

@@ -159,3 +159,37 @@ def test_block_norm_in_place_with_a_stride(moe):
     assert f(block(moe, **strided), P(1 << 16), DUMMY, None) == moe.ERR_INVALID_ARG
     assert f(block(moe, y=None, w_post=None, **strided), None, DUMMY, None) == moe.ERR_INVALID_ARG
     assert f(block(moe, w_next=None, **strided), DUMMY, None, None) == moe.ERR_INVALID_ARG
+
+
+def test_balance_misaligned_pointers(moe):
+    """Elements of four bytes at addresses of four (bytes of the mask anywhere)."""
+    odd = P(4098)
+    for name in ("scores", "ids", "off", "counts", "tokens", "loss"):
+        assert balance(moe, **{name: odd}) == moe.ERR_INVALID_ARG, name
+    for name in ("scores", "ids", "w", "dw", "off", "counts", "tokens", "gl", "out"):
+        assert router(moe, **{name: odd}) == moe.ERR_INVALID_ARG, name
+
+
+def test_block_norm_misaligned_pointers(moe):
+    """Elements of their own type's size."""
+    lib, bad = moe.load(), moe.ERR_INVALID_ARG
+    byte, half = 4097, 4098
+    a, b = P(1 << 16), P(1 << 17)
+    for kw in (dict(x=byte), dict(y=byte), dict(w_post=byte), dict(w_next=byte), dict(y=half, y_dtype=0),
+               dict(gate=byte, gate_kind=1), dict(gate=byte, gate_kind=3), dict(gate=half, gate_kind=2)):
+        assert lib.moe_block_norm(block(moe, **kw), a, b, None) == bad, kw
+        g = a if "gate" in kw else None
+        assert lib.moe_block_norm_backward(block(moe, **kw), a, a, b, b, g, a, a, a, 1 << 30, None) == bad, kw
+    assert lib.moe_block_norm(block(moe), P(byte), b, None) == bad
+    assert lib.moe_block_norm(block(moe), a, P(byte), None) == bad
+    good = dict(go=a, gn=a, dx=b, dy=b, dg=a, dwp=a, dwn=a)
+    for name, at, gate in (("go", byte, 1), ("gn", byte, 1), ("dx", byte, 1), ("dy", byte, 1), ("dg", half, 1),
+                           ("dg", half, 2), ("dg", byte, 3), ("dwp", half, 1), ("dwn", half, 1)):
+        p = {**good, name: P(at)}
+        assert lib.moe_block_norm_backward(block(moe, gate=4096, gate_kind=gate), p["go"], p["gn"], p["dx"], p["dy"],
+                                           p["dg"], p["dwp"], p["dwn"], a, 1 << 30, None) == bad, (name, gate)
+
+
+def test_w4_misaligned_routing(moe):
+    for kw in (dict(ids=P(4098)), dict(ids=DUMMY, wts=P(4098))):
+        assert w4(moe, num_mats=4, k=2, **kw) == moe.ERR_INVALID_ARG, kw
