@@ -378,8 +378,10 @@ moe_status moe_check_routing(const int32_t* topk_ids, int32_t T, int32_t k, int3
  *   counts device [S][E] int32, tokens device [S] int32, loss device [S][2] float32
  *   workspace   device, >= moe_balance_workspace_bytes(T, E, S), 16-byte aligned
  *               (NULL if that is 0)
- * All sums are FP32 in an order that depends on the sizes only: equal inputs
- * give equal bits.  T == 0 writes zeros.
+ * All sums are FP32, in an order that depends on the sizes, the GPU's number of
+ * CUs and whether E is a multiple of 4 and scores 16-byte aligned (the order of
+ * a row's softmax sum): calls alike in these give equal bits for equal inputs.
+ * T == 0 writes zeros.
  * Sizes: T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 64), S >= 1, else
  * MOE_ERR_INVALID_ARG, as for null pointers and ones that are no multiple of
  * their elements' size; T <= 2^30, S <= 2^20, T*k <= 2^31 - 1, else
@@ -406,8 +408,9 @@ moe_status moe_balance_loss(const float* scores, const int32_t* topk_ids,
  *   topk_weights, grad_weights  device [T][k] float32, or both NULL: no second line
  *                (topk_ids is then not read)
  *   grad_scores  device [T][E] float32
- * T == 0 is a no-op.  Sizes and errors as moe_balance_loss; with both
- * grad_loss and grad_weights NULL MOE_ERR_INVALID_ARG.
+ * T == 0 is a no-op.  Sizes, errors and the order of sums as moe_balance_loss
+ * (grad_scores' alignment counts too); with both grad_loss and grad_weights
+ * NULL MOE_ERR_INVALID_ARG.
  */
 moe_status moe_router_backward(const float* scores, const int32_t* topk_ids,
                                const float* topk_weights, const float* grad_weights,
@@ -459,7 +462,9 @@ typedef struct {
  * Sizes: 1 <= H <= 16384 (MOE_ERR_UNSUPPORTED past it), eps >= 0.  Rows are
  * read 16 bytes at a time when H and the strides are multiples of 8 and the
  * pointers 16-byte aligned, by element otherwise (pointers that are no multiple
- * of their elements' size are refused).
+ * of their elements' size are refused).  The order of a row's sums depends on H,
+ * on which of the two it is and, for H of 4097 to 8192, on whether T is past the
+ * GPU's number of CUs; not on the rows beside it, nor on T or the strides else.
  */
 moe_status moe_block_norm(const moe_block* B, void* out, void* n, void* stream);
 
@@ -475,7 +480,8 @@ moe_status moe_block_norm(const moe_block* B, void* out, void* n, void* stream);
  *               MOE_GATE_NONE
  *   grad_w_post, grad_w_next  device [H] float32, given exactly when the weights
  *               are: sums over the tokens, in FP32, in an order that depends on
- *               the sizes only (T == 0 writes zeros)
+ *               the sizes, the GPU's number of CUs and whether rows are read 16
+ *               bytes at a time, as the rows' own sums do (T == 0 writes zeros)
  *   workspace   device, >= moe_block_norm_backward_workspace_bytes(T, H) bytes,
  *               16-byte aligned; no contents kept between calls
  * Without y and without w_next there is nothing to differentiate:
