@@ -352,6 +352,11 @@ def check_routing(ids, num_experts, result=None, stream=None):
 
 
 # ---- operators around the layer ------------------------------------------
+#
+# As everywhere in this binding no call records an autograd graph: a result is
+# a constant to torch, whatever its inputs require, and the gradients are calls
+# of their own (router_backward, block_norm_backward), which a caller's
+# torch.autograd.Function can make.
 
 def _on_device(fn):
     """Run a binding call on its first tensor's device and, with `stream`,
@@ -413,7 +418,8 @@ def balance_loss(scores, ids, mask=None, seq_offsets=None):
     """Router statistics of scores [T][E] float32 and the routed ids [T][k]:
     (loss [S][2] float32 -- balance and z loss, counts [S][E] int32, tokens [S]
     int32).  mask [T] bool: tokens that count; seq_offsets [S+1] int32: the
-    sequences' bounds in T (default: one sequence of all tokens)."""
+    sequences' bounds in T (default: one sequence of all tokens).  The loss has
+    no autograd graph: its gradient is router_backward's."""
     load()
     _need(scores.dim() == 2 and ids.dim() == 2, "scores [T][E] and ids [T][k] are needed")
     t, e = scores.shape
@@ -509,7 +515,8 @@ def block_norm(x, y=None, w_post=None, w_next=None, gate=None, res_scale=1.0, ep
     the next block: (out, n) with out = res_scale x + gate (.) norm(y) w_post and
     n = norm(out) w_next.  Without y: (None, norm(x) w_next).  x, y [T][H] with
     any row stride; weights [H] and gate [H] (channels) or [T][H] in x's dtype,
-    or gate [T][1] float32 (tokens).  out may be x (in place)."""
+    or gate [T][1] float32 (tokens).  out may be x (in place).  The results have
+    no autograd graph: their gradient is block_norm_backward's."""
     load()
     _need(x.dim() == 2 and x.dtype in _ROWS, "x: bfloat16 or float32 rows [T][H] are needed")
     b, _ = _block(x, x, y, w_post, w_next, gate, res_scale, eps)
@@ -606,7 +613,8 @@ def w4_linear(W, x, ids=None, weights=None, swiglu=False, y=None, y_dtype="f32",
     """y [T][N] = x [T][K] times the transpose of W4Weights W's one matrix; with ids
     [T][k]: y [T][k][N] of the routed matrices, x [T][K] or [T][k][K].  swiglu:
     SiLU(first half) * second half of the outputs; weights [T][k] float32: slot
-    (t, j)'s outputs times its weight."""
+    (t, j)'s outputs times its weight.  y has no autograd graph, and there is no
+    backward pass."""
     return _w4_linear(x, W, ids, weights, swiglu, y, y_dtype, stream=stream)
 
 
