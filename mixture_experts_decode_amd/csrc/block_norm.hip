@@ -9,9 +9,9 @@
 // sums and statistics are FP32; o and n are each rounded once, n from the
 // unrounded o.
 //
-// 16384 x 4096, BF16 rows: forward 95 us (537 MB at 5.7 TB/s; a copy of 4 GiB
-// reaches 6.24), backward 153 + 6 us (806 MB at 5.1 TB/s).  One row of 2048:
-// 2.7 us, the latency of a load, two reductions and a store.
+// 16384 x 4096, BF16 rows: forward 96 us (537 MB at 5.6 TB/s; a copy of 4 GiB
+// reaches 6.24), backward 149 + 5 us (806 MB at 5.2 TB/s).  One row of 2048:
+// 2.9 us, the latency of a load, two reductions and a store.
 
 #include <algorithm>
 #include <cmath>
@@ -447,7 +447,8 @@ struct Shape {
 //   16384 x 4096   256 x 2: 94.6   1024 x 1: 129.3
 //    4096 x 7168   256 x 4: 43.6    512 x 2: 46.1    1024 x 1: 47.8   1024 x 2: 69.4
 // but 1024 x 1 for rows read by element (1000 x 8191: 19.2, 256 x 4: 26.1) and
-// for fewer rows than CUs (64 x 7168: 4.1, 256 x 4: 4.3).
+// for fewer rows than CUs (64 x 7168: 4.1, 256 x 4: 4.3).  Only 1024 x 2 spills
+// registers, read by element with y (85 to 117 of them).
 Shape shape_of(int H, int T, bool vec) {
   if (H <= 512) return {64, 1};
   if (H <= 2048) return {256, 1};
@@ -461,6 +462,9 @@ Shape shape_of(int H, int T, bool vec) {
 //    4096 x 2048   256 x 1: 33     256 x 2: 36
 //   16384 x 4096   256 x 2: 157    512 x 2: 235
 //     515 x 7168   512 x 2: 26     512 x 4: 182 (registers spilled to scratch)
+// 64 x 1 (128 registers a thread at 1024 threads) spills 5 to 30 of them with y,
+// and by element 83 to 103; 512 x 2 spills 17 in FP32 with y, and by element 139
+// to 172; 512 x 4 spills 226 to 331, and without y up to 59 or, by element, 279.
 Shape back_shape_of(int H) {
   if (H <= 512) return {64, 1};
   if (H <= 2048) return {256, 1};

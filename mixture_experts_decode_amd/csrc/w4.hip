@@ -16,10 +16,13 @@
 // use them they cost a cache line each: 84.6 us against 46.6 without them, for
 // the first product below).  Many short wavefronts keep the loads of a CU in
 // flight and even out by themselves; persistent workgroups with x in LDS and a
-// ring of steps in flight took 59 us.  What bounds it is the issue of vector
-// instructions, about 160 for 256 inputs of 16 rows (56 convert the codes, 48
-// finish four groups), 46% of the issue slots over the whole kernel, and the
-// waits around them: 51.0 us, 170.6 MB of weights and scales at 3.35 TB/s.
+// ring of steps in flight took 59 us.  40961 x 7168 for 5 rows: 51.0 us, 170.6 MB
+// of weights and scales at 3.35 TB/s, which no unit explains by itself: HBM is at
+// 54% of the copy rate and the vector unit busy for 46% of the time.  A wavefront
+// issues about 209 vector instructions for 256 inputs of 16 rows, some 160 in the
+// loop (56 convert the codes, 48 finish four groups), the rest before and after
+// it; x goes through L2 once for every 16 weight rows (1.69 M L2 hits beside
+// 1.35 M misses).  The time between is waits.
 //
 // A code becomes BF16 without a table: as an E4M3 byte the codes 0..15 stand
 // for 0..15 times 2^-9 (eight subnormals and the first binade), which the
