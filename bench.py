@@ -530,17 +530,30 @@ def main():
         "down_bytes_per_launch": round(main_res["down_bytes_per_launch"])
         if "down_bytes_per_launch" in main_res else None,
         "sweep": sweep,
-        "layers": layers_sweep,
+        "layers": [brief_layer(r) for r in layers_sweep],
         "roofline": roofline,
         "cpu_baseline": cpu,
         "accuracy": accuracy,
         "router": router,
         "grouped": grouped,
     }
-    print(json.dumps(out), flush=True)
+    print(json.dumps(out, separators=(",", ":")), flush=True)
 
 
 # ---------------------------------------------------------------------------
+
+def brief_layer(row):
+    """A row of the layer sweep as the JSON line holds it: each path's median time
+    and rates.  The whole row, with the spread of the replays and the parity
+    check, is on stderr; with the 21 whole rows the line was 23 KB long, more
+    than a reader that keeps the last 16 KB of the output can parse."""
+    out = {k: v for k, v in row.items() if k not in ("decode", "grouped", "entries", "algorithmic_MB")}
+    for path in ("decode", "grouped"):
+        if path in row:
+            e = row[path]
+            out[path] = {"us": e["us"]["p50"], **{k: v for k, v in e.items() if k not in ("us", "parity")}}
+    return out
+
 
 def rounded(r, keys):
     return {k: (round(r[k], 4) if isinstance(r[k], float) else r[k]) for k in keys if k in r}

@@ -94,3 +94,21 @@ def test_bench_helpers():
     assert bench.sample_rows(100, 3) == [0, 49, 99]
     s = bench.spread([3.0, 1.0, 2.0])
     assert s["p50"] == 2.0 and s["n"] == 3 and s["p10"] <= s["p50"] <= s["p90"]
+
+
+def test_bench_line_holds_brief_layers():
+    """A row's times and rates without what stands on stderr; 21 rows of both
+    paths in less than 6 KB."""
+    import json
+    import bench
+    path = {"us": {"p10": 250.94, "p50": 254.62, "p90": 261.48, "n": 5}, "TBps": 3.905,
+            "parity": {"tokens": 3, "mode": "mxfp8", "min_cos": 0.99999966, "max_rel_l2": 0.0008284,
+                       "max_abs": 0.007812, "pass": True},
+            "frac_of_copy_peak": 0.6254, "mfma_frac_useful": 0.0152}
+    row = {"workload": "deepseek_v3_fp8_blk128", "routing": "uniform", "B": 256, "entries": 2048, "auto": "grouped",
+           "touched_mean": 113.75, "algorithmic_MB": 1143.73, "decode": path, "grouped": path}
+    b = bench.brief_layer(row)
+    assert b["grouped"] == {"us": 254.62, "TBps": 3.905, "frac_of_copy_peak": 0.6254, "mfma_frac_useful": 0.0152}
+    assert b["B"] == 256 and b["auto"] == "grouped" and row["grouped"] is path
+    assert "decode" not in bench.brief_layer({k: v for k, v in row.items() if k != "decode"})
+    assert len(json.dumps([b] * 21, separators=(",", ":"))) < 6000
